@@ -336,6 +336,108 @@ W8A8_API w8a8_status w8a8_gemm_postscale_noalloc(const int8_t* Xq, const float* 
                                                  const float* sw, const void* bias, void* Y, int64_t M, int64_t N,
                                                  int64_t K, void* stream);
 
+/* Element types of the operators below that take more than one. */
+typedef enum { W8A8_BF16 = 0, W8A8_FP16 = 1, W8A8_FP32 = 2 } w8a8_dtype;
+
+/*
+ * Attention between a layer's Linears, over packed sequences: for sequence b
+ * with queries i (n of them) and keys j (m of them), query head h and KV head
+ * h / (Hq / Hk),
+ *   t_ij = scale * (q_i . k_j),   j < m and, with causal, j <= i + m - n
+ *          (the last query sees every key),
+ *   o_i  = sum_j exp(t_ij) v_j / sum_j exp(t_ij),  lse_i = log sum_j exp(t_ij);
+ * a query that sees no key gets o = 0 and lse = -inf, and no value of a key
+ * that a query does not see (infinities and NaN included) reaches its row.
+ * Products are summed, and the softmax and its output held, in binary32; the
+ * weights exp(t) enter the second product rounded to the inputs' type.
+ *   Q [Tq,Hq,D], K, V [Tk,Hk,D], O [Tq,Hq,D]: dtype BF16 or FP16, the last
+ *   dimension dense, token and head strides in elements (multiples of 8);
+ *   D % 8 == 0 and D <= 128, Hq % Hk == 0.  O must not overlap the inputs.
+ *   lse [Tq,Hq] fp32 out or NULL.
+ *   cu_q, cu_k [batch+1] int32 (device) or NULL: rows cu[b] .. cu[b+1] are
+ *   sequence b's; NULL: batch equal parts of Tq / Tk rows (else
+ *   W8A8_ERR_SHAPE).  k_lens [batch] int32 (device) or NULL: only the first
+ *   k_lens[b] rows of the part are keys (a cache that is not full).  Values
+ *   outside the tensors' rows are clamped to them.  Rows of O that belong to
+ *   no sequence are not written.
+ *   scale > 0, finite.
+ *   workspace: w8a8_attention_workspace_size() bytes, 256-byte aligned.  Its
+ *   first w8a8_attention_workspace_zeroed() bytes must be zero before its
+ *   first use; every call leaves them zero.  Calls that may overlap on the
+ *   GPU need a workspace each.
+ */
+W8A8_API size_t w8a8_attention_workspace_size(void);
+W8A8_API size_t w8a8_attention_workspace_zeroed(void);
+W8A8_API w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O, float* lse,
+                                    const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_lens,
+                                    w8a8_dtype dtype, int64_t batch, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                                    int64_t D, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                                    int64_t v_token, int64_t v_head, int64_t o_token, int64_t o_head, float scale,
+                                    int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum {
+    W8A8_ROTARY_HALF = 0,        /* pair k: elements k and k + rot/2 */
+    W8A8_ROTARY_INTERLEAVED = 1  /* pair k: elements 2k and 2k + 1   */
+} w8a8_rotary_layout;
+
+/*
+ * Rotary positions.  Pair k of every head of token t turns by the angle
+ * a = positions[t] * freqs[k] (minus that with inverse, which is also the
+ * gradient's direction): (x, y) -> amplitude * (x cos a - y sin a,
+ * y cos a + x sin a).  Elements past the first rot of a head are copied.  The
+ * angle is reduced exactly for any 64-bit position; cos and sin are binary32.
+ *   Q [T,Hq,D], K [T,Hk,D] (NULL with Hk = 0), Q_out, K_out: dtype BF16 or
+ *   FP16, last dimension dense, token and head strides in elements
+ *   (multiples of 8).  An output may be its input (same pointer and strides);
+ *   otherwise they must not overlap.  D % 8 == 0, D <= 256, rot % 16 == 0,
+ *   0 < rot <= D.
+ *   positions [T] int64, freqs [rot/2] fp64 (radians per position), device.
+ * w8a8_rotary_append also copies V and writes K and V to rows slots[t] (int64,
+ * device) of K_cache / V_cache [cache_rows,Hk,D]; a slot outside
+ * [0, cache_rows) (-1 for a padding token) stores nothing.  Two tokens with
+ * the same slot: either may win.
+ */
+W8A8_API w8a8_status w8a8_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
+                                 int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token, int64_t q_head,
+                                 int64_t k_token, int64_t k_head, int64_t qo_token, int64_t qo_head,
+                                 int64_t ko_token, int64_t ko_head, const int64_t* positions, const double* freqs,
+                                 float amplitude, w8a8_rotary_layout layout, int inverse, void* stream);
+W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void* Q_out, void* K_cache,
+                                        void* V_cache, w8a8_dtype dtype, int64_t T, int64_t Hq, int64_t Hk,
+                                        int64_t D, int64_t rot, int64_t cache_rows, int64_t q_token, int64_t q_head,
+                                        int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                                        int64_t qo_token, int64_t qo_head, int64_t kc_token, int64_t kc_head,
+                                        int64_t vc_token, int64_t vc_head, const int64_t* positions,
+                                        const int64_t* slots, const double* freqs, float amplitude,
+                                        w8a8_rotary_layout layout, void* stream);
+
+/*
+ * From one block's output to the next block's W8A8 Linear in one pass:
+ *   b' = B, or RMSNorm(B) * branch_gamma            (branch_gamma [K])
+ *   h  = alpha * X + gate * b'                      (gate absent: 1)
+ *   n  = RMSNorm or LayerNorm (kind) of h, times gamma, plus beta
+ *   y  = n * (1 + mod_scale) + mod_shift
+ *   sx[m] = max|y[m,:]| / 127, code = clamp(rne(y * (1 / sx[m])), -127, 127)
+ * in binary32 throughout: n is computed from the unrounded h and the codes
+ * from the unrounded y.  The statistics are those of w8a8_norm_quant (both
+ * norms use eps); the quantizer's conventions for an all-zero row are those
+ * of w8a8_quantize_act.
+ *   X, H [M,K] residual stream in / out, x_dtype BF16 or FP32 (H may be X);
+ *   B [M,K] bf16 the branch; branch_gamma, gamma, beta [K] bf16 or NULL;
+ *   gate, mod_scale, mod_shift bf16 or NULL: row m uses row m / rows_per_group,
+ *   whose rows lie mod_stride elements apart (a multiple of 8; rows_per_group
+ *   0: one row for all).
+ *   Outputs, each NULL where not wanted: Y [M,K] bf16; Xq [M,K] int8;
+ *   Ximg [M,K] bf16 (the codes' image, the GEMM's operand); sx [M] fp32,
+ *   required with Xq or Ximg.  K % 8 == 0, K <= 16384.
+ */
+W8A8_API w8a8_status w8a8_residual_norm_quant(const void* X, const void* B, void* H, w8a8_dtype x_dtype,
+                                              const void* branch_gamma, const void* gamma, const void* beta,
+                                              const void* gate, const void* mod_scale, const void* mod_shift,
+                                              int64_t mod_stride, int64_t rows_per_group, float alpha, float eps,
+                                              w8a8_norm_kind kind, int64_t M, int64_t K, void* Y, int8_t* Xq,
+                                              void* Ximg, float* sx, void* stream);
+
 /*
  * Test and debug exports of the same mainloops, stopping before the bf16
  * epilogue.

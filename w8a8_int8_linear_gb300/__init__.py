@@ -52,6 +52,13 @@ SIGNATURES = [
     ("w8a8_norm_quant", _I32, [_P, _P, _P, ctypes.c_float, ctypes.c_int, _I64, _I64, _P, _P, _P, _P, _P]),
     ("w8a8_splitk_workspace_size", _SZ, [_I64, _I64, _I64]),
     ("w8a8_gemm_postscale_images", _I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    ("w8a8_attention_workspace_size", _SZ, []),
+    ("w8a8_attention_workspace_zeroed", _SZ, []),
+    ("w8a8_attention", _I32, [_P] * 8 + [_I32] + [_I64] * 14 + [ctypes.c_float, _I32, _P, _SZ, _P]),
+    ("w8a8_rotary", _I32, [_P] * 4 + [_I32] + [_I64] * 13 + [_P, _P, ctypes.c_float, _I32, _I32, _P]),
+    ("w8a8_rotary_append", _I32, [_P] * 6 + [_I32] + [_I64] * 18 + [_P, _P, _P, ctypes.c_float, _I32, _P]),
+    ("w8a8_residual_norm_quant", _I32, [_P, _P, _P, _I32] + [_P] * 6 + [_I64, _I64, ctypes.c_float, ctypes.c_float,
+                                                                        _I32, _I64, _I64, _P, _P, _P, _P, _P]),
     ("w8a8_gemm_postscale_noalloc", _I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     ("w8a8_gemm_postscale_s32", _I32, [_P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     ("w8a8_gemm_blockwise_f32", _I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
@@ -522,5 +529,7 @@ def measure_imma_peak():
     return v.value
 
 
+from .operators import HALF, INTERLEAVED, attention, residual_norm_quant, rotary, rotary_append, \
+    rotary_frequencies  # noqa: E402
 from .module import Int8FFN, Int8Linear
 from .pipeline import HostPipeline  # noqa: E402  (the modules use the functions above)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdint>
@@ -46,6 +47,7 @@ w8a8_status cuda_fail(const char* what, cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Workspace of the GEMM on bf16 operand images: the images of Xq and Wq and
@@ -596,6 +598,202 @@ w8a8_status w8a8_gemm_blockwise_f32(const int8_t* Xq, const float* sx, const int
     if (s != W8A8_OK || none) return s;
     return run_gemm(w8a8::kEpiBlockwiseF32, Xq, sx, Wq, sw, nullptr, acc, M, N, K, workspace, dev,
                     static_cast<cudaStream_t>(stream));
+}
+
+size_t w8a8_attention_workspace_size(void) {
+    DeviceInfo dev;
+    return current_device(&dev) == W8A8_OK ? w8a8::attention_workspace_bytes(dev.num_sms) : 0;
+}
+
+size_t w8a8_attention_workspace_zeroed(void) {
+    DeviceInfo dev;
+    return current_device(&dev) == W8A8_OK ? w8a8::attention_counter_bytes(dev.num_sms) : 0;
+}
+
+w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O, float* lse, const int32_t* cu_q,
+                           const int32_t* cu_k, const int32_t* k_lens, w8a8_dtype dtype, int64_t batch, int64_t Tq,
+                           int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t q_token, int64_t q_head,
+                           int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int64_t o_token,
+                           int64_t o_head, float scale, int causal, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
+    if (batch < 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return W8A8_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
+    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || Tk > INT32_MAX || batch > INT32_MAX)
+        return W8A8_ERR_SHAPE;
+    if (batch == 0 || Tq == 0) return W8A8_OK;
+    if ((!cu_q && Tq % batch != 0) || (!cu_k && Tk % batch != 0)) return W8A8_ERR_SHAPE;
+    if (!Q || !O || (Tk > 0 && (!K || !V))) return W8A8_ERR_INVALID_ARG;
+    const int64_t strides[8] = {q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head};
+    for (int64_t v : strides)
+        if (v < 0 || v % 8 != 0) return W8A8_ERR_ALIGNMENT;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lse) || !aligned4(cu_q) ||
+        !aligned4(cu_k) || !aligned4(k_lens))
+        return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    w8a8_status s = current_device(&dev);
+    if (s != W8A8_OK) return s;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < w8a8::attention_workspace_bytes(dev.num_sms))
+        return W8A8_ERR_WORKSPACE;
+    w8a8::AttentionArgs a{};
+    a.q = Q;
+    a.k = K;
+    a.v = V;
+    a.o = O;
+    a.lse = lse;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.k_lens = k_lens;
+    a.batch = static_cast<int>(batch);
+    a.Tq = static_cast<int>(Tq);
+    a.Tk = static_cast<int>(Tk);
+    a.Hq = static_cast<int>(Hq);
+    a.Hk = static_cast<int>(Hk);
+    a.D = static_cast<int>(D);
+    a.group = static_cast<int>(Hq / Hk);
+    a.q_token = q_token;
+    a.q_head = q_head;
+    a.k_token = k_token;
+    a.k_head = k_head;
+    a.v_token = v_token;
+    a.v_head = v_head;
+    a.o_token = o_token;
+    a.o_head = o_head;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.causal = causal != 0;
+    return from_cuda(w8a8::launch_attention(a, dtype, dev.num_sms, workspace, static_cast<cudaStream_t>(stream)),
+                     "attention launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks and launch shared by the two rotary entry points.
+w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_layout layout, int64_t D, int64_t rot,
+                       cudaStream_t st) {
+    if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
+    if (layout != W8A8_ROTARY_HALF && layout != W8A8_ROTARY_INTERLEAVED) return W8A8_ERR_INVALID_ARG;
+    if (a.tokens < 0 || a.cache_rows < 0 || a.q.heads < 0 || a.k.heads < 0 || D <= 0 || rot <= 0)
+        return W8A8_ERR_INVALID_ARG;
+    if (!(fabsf(a.amplitude) <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > 256 || rot % 16 != 0 || rot > D || a.tokens > INT32_MAX) return W8A8_ERR_SHAPE;
+    if (a.tokens == 0 || (a.q.heads == 0 && a.k.heads == 0)) return W8A8_OK;
+    if (!a.positions || !a.freqs) return W8A8_ERR_INVALID_ARG;
+    const w8a8::Heads* sides[6] = {&a.q, &a.q_out, &a.k, &a.k_out, &a.v, &a.v_out};
+    for (const w8a8::Heads* h : sides) {
+        if (h->heads == 0) continue;
+        if (!h->ptr) return W8A8_ERR_INVALID_ARG;
+        if (h->token < 0 || h->head < 0 || h->token % 8 != 0 || h->head % 8 != 0 || !aligned16(h->ptr))
+            return W8A8_ERR_ALIGNMENT;
+    }
+    if ((reinterpret_cast<uintptr_t>(a.positions) & 7u) || (reinterpret_cast<uintptr_t>(a.slots) & 7u) ||
+        (reinterpret_cast<uintptr_t>(a.freqs) & 7u))
+        return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    w8a8_status s = current_device(&dev);
+    if (s != W8A8_OK) return s;
+    return from_cuda(w8a8::launch_rotary(a, dtype, layout == W8A8_ROTARY_HALF, st), "rotary launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+w8a8_status w8a8_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
+                        int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token, int64_t q_head,
+                        int64_t k_token, int64_t k_head, int64_t qo_token, int64_t qo_head, int64_t ko_token,
+                        int64_t ko_head, const int64_t* positions, const double* freqs, float amplitude,
+                        w8a8_rotary_layout layout, int inverse, void* stream) {
+    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
+    const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
+    w8a8::RotaryArgs a{};
+    a.q = {Q, q_token, q_head, hq};
+    a.q_out = {Q_out, qo_token, qo_head, hq};
+    a.k = {K, k_token, k_head, hk};
+    a.k_out = {K_out, ko_token, ko_head, hk};
+    a.positions = positions;
+    a.tokens = T;
+    a.freqs = freqs;
+    a.dim = static_cast<int>(D);
+    a.rot = static_cast<int>(rot);
+    a.inverse = inverse != 0;
+    a.amplitude = amplitude;
+    return run_rotary(a, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache,
+                               w8a8_dtype dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
+                               int64_t cache_rows, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                               int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head, int64_t kc_token,
+                               int64_t kc_head, int64_t vc_token, int64_t vc_head, const int64_t* positions,
+                               const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
+                               void* stream) {
+    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
+    if (Hk <= 0) return W8A8_ERR_INVALID_ARG;
+    if (T > 0 && !slots) return W8A8_ERR_INVALID_ARG;
+    const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
+    w8a8::RotaryArgs a{};
+    a.q = {Q, q_token, q_head, hq};
+    a.q_out = {Q_out, qo_token, qo_head, hq};
+    a.k = {K, k_token, k_head, hk};
+    a.k_out = {K_cache, kc_token, kc_head, hk};
+    a.v = {V, v_token, v_head, hk};
+    a.v_out = {V_cache, vc_token, vc_head, hk};
+    a.positions = positions;
+    a.slots = slots;
+    a.tokens = T;
+    a.cache_rows = cache_rows;
+    a.freqs = freqs;
+    a.dim = static_cast<int>(D);
+    a.rot = static_cast<int>(rot);
+    a.amplitude = amplitude;
+    return run_rotary(a, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status w8a8_residual_norm_quant(const void* X, const void* B, void* H, w8a8_dtype x_dtype,
+                                     const void* branch_gamma, const void* gamma, const void* beta, const void* gate,
+                                     const void* mod_scale, const void* mod_shift, int64_t mod_stride,
+                                     int64_t rows_per_group, float alpha, float eps, w8a8_norm_kind kind, int64_t M,
+                                     int64_t K, void* Y, int8_t* Xq, void* Ximg, float* sx, void* stream) {
+    if (x_dtype != W8A8_BF16 && x_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (kind != W8A8_NORM_RMS && kind != W8A8_NORM_LAYER) return W8A8_ERR_INVALID_ARG;
+    if (M < 0 || K <= 0 || rows_per_group < 0 || mod_stride < 0) return W8A8_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(fabsf(alpha) <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
+    if (K % 8 != 0 || K > 16384 || M > INT32_MAX) return W8A8_ERR_SHAPE;
+    if (M == 0) return W8A8_OK;
+    if (!X || !B || !H || ((Xq || Ximg) && !sx) || (sx && !Xq && !Ximg)) return W8A8_ERR_INVALID_ARG;
+    const void* vectors[13] = {X, B, H, branch_gamma, gamma, beta, gate, mod_scale, mod_shift, Y, Xq, Ximg, sx};
+    for (const void* v : vectors)
+        if (!aligned16(v)) return W8A8_ERR_ALIGNMENT;
+    if (mod_stride % 8 != 0) return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    w8a8_status s = current_device(&dev);
+    if (s != W8A8_OK) return s;
+    w8a8::ResidualNormArgs a{};
+    a.X = X;
+    a.B = B;
+    a.H = H;
+    a.branch_gamma = branch_gamma;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.gate = gate;
+    a.mod_scale = mod_scale;
+    a.mod_shift = mod_shift;
+    a.mod_stride = mod_stride;
+    a.rows_per_group = rows_per_group;
+    a.M = M;
+    a.K = K;
+    a.alpha = alpha;
+    a.eps = eps;
+    a.layer = kind == W8A8_NORM_LAYER;
+    a.Y = Y;
+    a.Xq = Xq;
+    a.Ximg = Ximg;
+    a.sx = sx;
+    return from_cuda(w8a8::launch_residual_norm(a, x_dtype == W8A8_FP32, static_cast<cudaStream_t>(stream)),
+                     "residual norm launch");
 }
 
 w8a8_status w8a8_gelu_bf16(const void* Y, int64_t n, void* G, void* stream) {

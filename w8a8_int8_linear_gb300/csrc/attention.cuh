@@ -1,0 +1,111 @@
+// What the attention kernels share: the sequences' bounds as the device holds
+// them, and warp-level tensor-core and copy building blocks.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace w8a8 {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Sequence b: queries [q0, q0 + n) and keys [k0, k0 + m) of the packed rows.
+// Offsets and lengths come from device memory and are clamped to the tensors'
+// rows, so that no value in them can make a kernel read or write out of range.
+struct Sequence {
+    int q0, n, k0, m;
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+__device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
+    Sequence s;
+    if (p.cu_q) {
+        s.q0 = clampi(p.cu_q[b], 0, p.Tq);
+        s.n = clampi(p.cu_q[b + 1], s.q0, p.Tq) - s.q0;
+    } else {
+        s.n = p.Tq / p.batch;
+        s.q0 = b * s.n;
+    }
+    if (p.cu_k) {
+        s.k0 = clampi(p.cu_k[b], 0, p.Tk);
+        s.m = clampi(p.cu_k[b + 1], s.k0, p.Tk) - s.k0;
+    } else {
+        s.m = p.Tk / p.batch;
+        s.k0 = b * s.m;
+    }
+    if (p.k_lens) s.m = clampi(p.k_lens[b], 0, s.m);
+    return s;
+}
+
+// 16 bytes global -> shared, asynchronously; zeros where `take` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    const int bytes = take ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// d (16 x 8, binary32) += a (16 x 16) b (16 x 8).
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Whether any of the eight 16-bit floats in w is infinite or NaN (all
+// exponent bits set).
+template <typename T>
+__device__ __forceinline__ bool any_non_finite(const uint4& w) {
+    const uint32_t e = sizeof(T) && (std::is_same<T, __half>::value) ? 0x7C00u : 0x7F80u;
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (u[i] & e) == e || ((u[i] >> 16) & e) == e;
+    return bad;
+}
+
+}  // namespace
+}  // namespace w8a8
