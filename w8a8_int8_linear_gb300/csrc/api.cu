@@ -662,8 +662,17 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
     a.o_head = o_head;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.causal = causal != 0;
-    return from_cuda(w8a8::launch_attention(a, dtype, dev.num_sms, workspace, static_cast<cudaStream_t>(stream)),
-                     "attention launch");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (Tq * a.group >= 32 * batch && w8a8::attention_prompt_takes(a)) {
+        void* enc = encode_fn();
+        if (!enc) return W8A8_ERR_CUDA;
+        t_detail[0] = 0;
+        const cudaError_t e = w8a8::launch_attention_prompt(a, dtype, enc, st, t_detail, sizeof t_detail);
+        if (e == cudaSuccess) return W8A8_OK;
+        cudaGetLastError();
+        return t_detail[0] ? W8A8_ERR_CUDA : cuda_fail("attention launch", e);
+    }
+    return from_cuda(w8a8::launch_attention(a, dtype, dev.num_sms, workspace, st), "attention launch");
 }
 
 }  // extern "C"
@@ -819,8 +828,11 @@ w8a8_status w8a8_get_device_error(int* code) {
     if (w8a8::gemm_read_device_error(&v) != cudaSuccess) return W8A8_ERR_CUDA;
     if (w8a8::gemm_s8_read_device_error(&vs) != cudaSuccess) return W8A8_ERR_CUDA;
     if (w8a8::quant_read_device_error(&vq) != cudaSuccess) return W8A8_ERR_CUDA;
+    unsigned int va = 0;
+    if (w8a8::attention_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
     if (v == 0) v = vs;
     if (v == 0) v = vq;
+    if (v == 0) v = va;
     *code = static_cast<int>(v);
     if (v >= w8a8::kDeviceErrorTimeoutBase) return W8A8_ERR_TIMEOUT;
     return v ? W8A8_ERR_CUDA : W8A8_OK;

@@ -118,6 +118,13 @@ size_t attention_workspace_bytes(int num_sms);
 // before the first call; every call leaves them zero.
 size_t attention_counter_bytes(int num_sms);
 cudaError_t launch_attention(const AttentionArgs& a, int dtype, int num_sms, void* workspace, cudaStream_t st);
+// The tensor-core kernel for many queries per sequence, on the calls it
+// takes; `encode_fn` is the driver's cuTensorMapEncodeTiled.  On failure a
+// one-line description is written to `detail` (size `n`).
+bool attention_prompt_takes(const AttentionArgs& a);
+cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, void* encode_fn, cudaStream_t st, char* detail,
+                                    size_t n);
+cudaError_t attention_read_device_error(unsigned int* code);
 
 // One [rows, heads, dim] side of the rotary kernel; strides count elements.
 struct Heads {
