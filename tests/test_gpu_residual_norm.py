@@ -66,7 +66,9 @@ CASES = [
     (33, 5120, "rms", BF16, False, True, False, None, 1.0), (4, 5120, "rms", BF16, True, True, False, None, 0.5),
     (10, 4096, "layer", torch.float32, False, False, False, 3, 1.0), (9, 8192, "layer", torch.float32, True, True, True, 4, -1.5),
     (6, 8200, "rms", BF16, False, True, True, 2, 1.0), (2, 16384, "layer", BF16, True, True, False, None, 1.0),
-    (257, 1000, "rms", BF16, True, True, False, 5, 0.25), (1, 16384, "rms", torch.float32, False, True, False, 1, 1.0),
+    (257, 1000, "rms", BF16, True, True, False, 5, 0.25), (2500, 1000, "layer", BF16, True, True, True, 7, 1.0),
+    (1300, 5120, "rms", BF16, True, True, False, None, 1.0), (1111, 8192, "layer", torch.float32, False, True, True, 2, 0.5),
+    (700, 16384, "rms", torch.float32, True, True, False, 2, 1.0), (3001, 64, "rms", BF16, False, True, False, None, 1.0), (1, 16384, "rms", torch.float32, False, True, False, 1, 1.0),
 ]
 
 

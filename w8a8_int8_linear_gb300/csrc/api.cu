@@ -801,7 +801,7 @@ w8a8_status w8a8_residual_norm_quant(const void* X, const void* B, void* H, w8a8
     a.Xq = Xq;
     a.Ximg = Ximg;
     a.sx = sx;
-    return from_cuda(w8a8::launch_residual_norm(a, x_dtype == W8A8_FP32, static_cast<cudaStream_t>(stream)),
+    return from_cuda(w8a8::launch_residual_norm(a, x_dtype == W8A8_FP32, dev.num_sms, static_cast<cudaStream_t>(stream)),
                      "residual norm launch");
 }
 
@@ -828,11 +828,13 @@ w8a8_status w8a8_get_device_error(int* code) {
     if (w8a8::gemm_read_device_error(&v) != cudaSuccess) return W8A8_ERR_CUDA;
     if (w8a8::gemm_s8_read_device_error(&vs) != cudaSuccess) return W8A8_ERR_CUDA;
     if (w8a8::quant_read_device_error(&vq) != cudaSuccess) return W8A8_ERR_CUDA;
-    unsigned int va = 0;
+    unsigned int va = 0, vr = 0;
     if (w8a8::attention_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
+    if (w8a8::residual_norm_read_device_error(&vr) != cudaSuccess) return W8A8_ERR_CUDA;
     if (v == 0) v = vs;
     if (v == 0) v = vq;
     if (v == 0) v = va;
+    if (v == 0) v = vr;
     *code = static_cast<int>(v);
     if (v >= w8a8::kDeviceErrorTimeoutBase) return W8A8_ERR_TIMEOUT;
     return v ? W8A8_ERR_CUDA : W8A8_OK;

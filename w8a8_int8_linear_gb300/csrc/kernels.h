@@ -158,7 +158,8 @@ struct ResidualNormArgs {
     void* Ximg;
     float* sx;
 };
-cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool f32, int num_sms, cudaStream_t st);
+cudaError_t residual_norm_read_device_error(unsigned int* code);
 
 // Device error codes at or above this value mean a bounded wait ran out.
 constexpr unsigned int kDeviceErrorTimeoutBase = 0x100;

@@ -16,7 +16,12 @@
 // Everything between the loads and the stores is binary32: the norm goes on
 // from the unrounded h, and the quantization takes the unrounded y (rounding
 // either to bf16 first would only add its half step, 2^-8, to the error).
-// One CTA per row; the row stays in registers between the reductions.
+//
+// Bytes bound it (read x and b, write h and y or the image: 8 bytes an
+// element), and a row passes two to four reductions over the CTA between its
+// loads and its stores.  With many rows a CTA therefore takes rows in a loop
+// and bulk copies keep its next rows on the way to shared memory while it
+// works on the present one; with few rows each CTA loads its row directly.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -71,167 +76,272 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(P16::pack(v[0], v[1]), P16::pack(v[2], v[3]), P16::pack(v[4], v[5]), P16::pack(v[6], v[7]));
 }
 
-// C chunks of 8 elements per thread, chunk threadIdx.x + i * blockDim.x.
-template <int C, bool kF32>
-__global__ void __launch_bounds__(256) residual_norm_kernel(const ResidualNormArgs p) {
-    __shared__ float red[4][32];
-    const int64_t row = blockIdx.x;
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = P16::unpack(u[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+constexpr int kMaxStages = 4;
+constexpr int kRingBytes = 200 * 1024;
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...: C chunks of 8 elements per
+// thread, chunk threadIdx.x + i * blockDim.x.  kRing: rows come through
+// `stages` shared-memory buffers (x, then b), else straight from memory.
+template <int C, bool kF32, bool kRing>
+__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNormArgs p, int stages) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][4][32];
+    __shared__ uint64_t full[kMaxStages];
+    constexpr int kXBytes = kF32 ? 4 : 2;
     const int chunks = static_cast<int>(p.K >> 3);
-    const int64_t base = row * chunks;
-    const int64_t group = p.rows_per_group ? row / p.rows_per_group : 0;
-    const int64_t mod = group * (p.mod_stride >> 3);
+    const uint32_t x_bytes = static_cast<uint32_t>(p.K) * kXBytes, b_bytes = static_cast<uint32_t>(p.K) * 2;
     const float inv_k = 1.0f / static_cast<float>(p.K);
-    float h[C][8];
-    float x[C][8];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = x[i][j] = 0.0f;
-        if (c >= chunks) continue;
-        load8(p.B, base + c, h[i]);
-        if (kF32) {
-            const float4* s = static_cast<const float4*>(p.X) + 2 * (base + c);
-            const float4 u = s[0], v = s[1];
-            x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
-            x[i][4] = v.x; x[i][5] = v.y; x[i][6] = v.z; x[i][7] = v.w;
-        } else {
-            // not through the read-only path: H may be X itself
-            const uint4 w = static_cast<const uint4*>(p.X)[base + c];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = P16::unpack(u[j]);
-                x[i][2 * j] = f.x;
-                x[i][2 * j + 1] = f.y;
+
+    auto fetch = [&](int64_t row, int st) {
+        uint8_t* dst = ring + static_cast<size_t>(st) * (x_bytes + b_bytes);
+        mbar_arrive_expect_tx(&full[st], x_bytes + b_bytes);
+        bulk_load(dst, static_cast<const uint8_t*>(p.X) + row * x_bytes, x_bytes, &full[st]);
+        bulk_load(dst + x_bytes, static_cast<const uint8_t*>(p.B) + row * b_bytes, b_bytes, &full[st]);
+    };
+    if (kRing) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+            fence_mbarrier_init();
+            for (int i = 0; i < stages; ++i) {
+                const int64_t row = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+                if (row < p.M) fetch(row, i);
             }
         }
+        __syncthreads();
     }
-    if (p.branch_gamma) {
+
+    int st = 0, phase = 0, odd = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, odd ^= 1) {
+        const int64_t base = row * chunks;
+        const int64_t group = p.rows_per_group ? row / p.rows_per_group : 0;
+        const int64_t mod = group * (p.mod_stride >> 3);
+        float h[C][8], x[C][8];
+        if (kRing && !mbar_wait(&full[st], phase, 80)) {
+            // recorded; the copies still on their way land before the CTA ends
+            if (threadIdx.x == 0)
+                for (int i = 1; i < stages; ++i) {
+                    const int at = (st + i) % stages;
+                    if (row + static_cast<int64_t>(i) * gridDim.x < p.M)
+                        mbar_wait(&full[at], at > st ? phase : phase ^ 1, 80);
+                }
+            return;
+        }
+        const uint8_t* buf = ring + static_cast<size_t>(st) * (x_bytes + b_bytes);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] = x[i][j] = 0.0f;
+            if (c >= chunks) continue;
+            // x not through the read-only path: H may be X itself
+            const uint4* xs = kRing ? reinterpret_cast<const uint4*>(buf)
+                                    : reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.X) + row * x_bytes);
+            const uint4* bs = kRing ? reinterpret_cast<const uint4*>(buf + x_bytes)
+                                    : reinterpret_cast<const uint4*>(p.B) + base;
+            if (kF32) {
+                const uint4 u = xs[2 * c], w = xs[2 * c + 1];
+                x[i][0] = __uint_as_float(u.x); x[i][1] = __uint_as_float(u.y);
+                x[i][2] = __uint_as_float(u.z); x[i][3] = __uint_as_float(u.w);
+                x[i][4] = __uint_as_float(w.x); x[i][5] = __uint_as_float(w.y);
+                x[i][6] = __uint_as_float(w.z); x[i][7] = __uint_as_float(w.w);
+            } else {
+                unpack8(xs[c], x[i]);
+            }
+            unpack8(bs[c], h[i]);
+        }
+        bool fetched = !kRing;
+        // after the first reduction's barrier every thread has read its part of
+        // the buffer: the row that goes there next can be fetched
+        auto refill = [&]() {
+            if (!fetched && threadIdx.x == 0) {
+                const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
+                if (next < p.M) fetch(next, st);
+            }
+            fetched = true;
+        };
+        if (p.branch_gamma) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+            const float r = __frcp_rn(__fsqrt_rn(fmaf(block_reduce<false>(s, red[odd][0]), inv_k, p.eps)));
+            refill();
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c >= chunks) continue;
+                float g[8];
+                load8(p.branch_gamma, c, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * r * g[j];
+            }
+        }
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c >= chunks) continue;
+            if (p.gate) {
+                float g[8];
+                load8(p.gate, mod + c, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
-        const float r = __frcp_rn(__fsqrt_rn(fmaf(block_reduce<false>(s, red[0]), inv_k, p.eps)));
+                for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * g[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] = fmaf(p.alpha, x[i][j], h[i][j]);
+            if (p.layer) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += h[i][j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+            }
+            if (kF32) {
+                float4* d = static_cast<float4*>(p.H) + 2 * (base + c);
+                d[0] = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
+                d[1] = make_float4(h[i][4], h[i][5], h[i][6], h[i][7]);
+            } else {
+                static_cast<uint4*>(p.H)[base + c] = pack8(h[i]);
+            }
+        }
+        s = block_reduce<false>(s, red[odd][1]);
+        refill();
+        float mu = 0.0f;
+        if (p.layer) {  // the variance about the mean, from the values in registers
+            mu = s * inv_k;
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (static_cast<int>(threadIdx.x + i * blockDim.x) >= chunks) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j] - mu, h[i][j] - mu, s);
+            }
+            s = block_reduce<false>(s, red[odd][2]);
+        }
+        const float r = __frcp_rn(__fsqrt_rn(fmaf(s, inv_k, p.eps)));
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= chunks) continue;
             float g[8];
-            load8(p.branch_gamma, c, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * r * g[j];
-        }
-    }
-    float s = 0.0f;
+            for (int j = 0; j < 8; ++j) h[i][j] = (h[i][j] - mu) * r;
+            if (p.gamma) {
+                load8(p.gamma, c, g);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= chunks) continue;
-        if (p.gate) {
-            float g[8];
-            load8(p.gate, mod + c, g);
+                for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
+            }
+            if (p.beta) {
+                load8(p.beta, c, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * g[j];
-        }
+                for (int j = 0; j < 8; ++j) h[i][j] += g[j];
+            }
+            if (p.mod_scale) {
+                load8(p.mod_scale, mod + c, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            h[i][j] = fmaf(p.alpha, x[i][j], h[i][j]);
-            s += p.layer ? h[i][j] : h[i][j] * h[i][j];
+                for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j], g[j], h[i][j]);
+            }
+            if (p.mod_shift) {
+                load8(p.mod_shift, mod + c, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] += g[j];
+            }
+            if (p.Y) static_cast<uint4*>(p.Y)[base + c] = pack8(h[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
         }
-        if (kF32) {
-            float4* d = static_cast<float4*>(p.H) + 2 * (base + c);
-            d[0] = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
-            d[1] = make_float4(h[i][4], h[i][5], h[i][6], h[i][7]);
-        } else {
-            static_cast<uint4*>(p.H)[base + c] = pack8(h[i]);
+        if (kRing && ++st == stages) {
+            st = 0;
+            phase ^= 1;
         }
-    }
-    s = block_reduce<false>(s, red[1]);
-    float mu = 0.0f;
-    if (p.layer) {  // the variance about the mean, from the values in registers
-        mu = s * inv_k;
-        s = 0.0f;
+        if (!p.sx) continue;
+        const RowScale sc = make_scale_div(block_reduce<true>(top, red[odd][3]));
+        if (threadIdx.x == 0) p.sx[row] = sc.s;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            if (static_cast<int>(threadIdx.x + i * blockDim.x) >= chunks) continue;
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c >= chunks) continue;
+            float q[8];
+            if (sc.exact) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(h[i][j] - mu, h[i][j] - mu, s);
-        }
-        s = block_reduce<false>(s, red[2]);
-    }
-    const float r = __frcp_rn(__fsqrt_rn(fmaf(s, inv_k, p.eps)));
-    float top = 0.0f;
+                for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(quant_exact(h[i][j], sc.s));
+            } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= chunks) continue;
-        float g[8];
+                for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(rintf(h[i][j] * sc.inv), -kQMax), kQMax);
+            }
+            if (p.Ximg) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = (h[i][j] - mu) * r;
-        if (p.gamma) {
-            load8(p.gamma, c, g);
+                for (int j = 0; j < 8; ++j) q[j] += 0.0f;  // the code 0 has one image, +0
+                static_cast<uint4*>(p.Ximg)[base + c] = pack8(q);
+            }
+            if (p.Xq) {
+                uint32_t w[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
-        }
-        if (p.beta) {
-            load8(p.beta, c, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] += g[j];
-        }
-        if (p.mod_scale) {
-            load8(p.mod_scale, mod + c, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j], g[j], h[i][j]);
-        }
-        if (p.mod_shift) {
-            load8(p.mod_shift, mod + c, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] += g[j];
-        }
-        if (p.Y) static_cast<uint4*>(p.Y)[base + c] = pack8(h[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
-    }
-    if (!p.sx) return;
-    const RowScale sc = make_scale_div(block_reduce<true>(top, red[3]));
-    if (threadIdx.x == 0) p.sx[row] = sc.s;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= chunks) continue;
-        float q[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q[j] = sc.exact ? static_cast<float>(quant_exact(h[i][j], sc.s))
-                            : fminf(fmaxf(rintf(h[i][j] * sc.inv), -kQMax), kQMax);
-        if (p.Ximg) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] += 0.0f;  // the code 0 has one image, +0
-            static_cast<uint4*>(p.Ximg)[base + c] = pack8(q);
-        }
-        if (p.Xq) {
-            uint32_t w[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j >> 2] |= (static_cast<uint32_t>(static_cast<int>(q[j])) & 0xFFu) << (8 * (j & 3));
-            reinterpret_cast<uint2*>(p.Xq)[base + c] = make_uint2(w[0], w[1]);
+                for (int j = 0; j < 8; ++j)
+                    w[j >> 2] |= (static_cast<uint32_t>(static_cast<int>(q[j])) & 0xFFu) << (8 * (j & 3));
+                reinterpret_cast<uint2*>(p.Xq)[base + c] = make_uint2(w[0], w[1]);
+            }
         }
     }
 }
 
+template <int C, bool kF32>
+cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st) {
+    const int chunks = static_cast<int>(a.K >> 3);
+    const int threads = 32 * ((chunks + 32 * C - 1) / (32 * C));
+    const int row_bytes = static_cast<int>(a.K) * (kF32 ? 6 : 4);
+    // CTAs that fit an SM by their threads (64 registers each), and two to four
+    // row buffers for each in 200 KB
+    int per_sm = 1024 / threads;
+    if (per_sm > 6) per_sm = 6;
+    while (per_sm > 1 && per_sm * 2 * row_bytes > kRingBytes) --per_sm;
+    int stages = kRingBytes / (per_sm * row_bytes);
+    if (stages > 4) stages = 4;
+    if (a.M <= static_cast<int64_t>(num_sms) * per_sm) {
+        residual_norm_kernel<C, kF32, false><<<static_cast<unsigned>(a.M), threads, 0, st>>>(a, 0);
+        return cudaGetLastError();
+    }
+    const size_t smem = static_cast<size_t>(stages) * row_bytes;
+    static int allowed[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || allowed[dev] == 0) {
+        e = cudaFuncSetAttribute(residual_norm_kernel<C, kF32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 208 * 1024);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev] = 1;
+    }
+    residual_norm_kernel<C, kF32, true><<<num_sms * per_sm, threads, smem, st>>>(a, stages);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool f32, cudaStream_t st) {
-    const int chunks = static_cast<int>(a.K >> 3);
-    const dim3 grid(static_cast<unsigned>(a.M));
-    auto threads = [&](int c) { return 32 * ((chunks + 32 * c - 1) / (32 * c)); };
-    auto launch = [&](auto kern, int c) { kern<<<grid, threads(c), 0, st>>>(a); };
-    if (chunks <= 256) f32 ? launch(residual_norm_kernel<1, true>, 1) : launch(residual_norm_kernel<1, false>, 1);
-    else if (chunks <= 1024) f32 ? launch(residual_norm_kernel<4, true>, 4) : launch(residual_norm_kernel<4, false>, 4);
-    else f32 ? launch(residual_norm_kernel<8, true>, 8) : launch(residual_norm_kernel<8, false>, 8);
-    return cudaGetLastError();
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool f32, int num_sms, cudaStream_t st) {
+    if (a.K <= 2048) return f32 ? launch_rows<1, true>(a, num_sms, st) : launch_rows<1, false>(a, num_sms, st);
+    return f32 ? launch_rows<2, true>(a, num_sms, st) : launch_rows<2, false>(a, num_sms, st);
+}
+
+cudaError_t residual_norm_read_device_error(unsigned int* code) {
+    unsigned int v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
+    *code = v;
+    return e;
 }
 
 }  // namespace w8a8
