@@ -667,7 +667,8 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
         void* enc = encode_fn();
         if (!enc) return W8A8_ERR_CUDA;
         t_detail[0] = 0;
-        const cudaError_t e = w8a8::launch_attention_prompt(a, dtype, enc, st, t_detail, sizeof t_detail);
+        const cudaError_t e = w8a8::launch_attention_prompt(a, dtype, dev.num_sms, workspace, enc, st, t_detail,
+                                                            sizeof t_detail);
         if (e == cudaSuccess) return W8A8_OK;
         cudaGetLastError();
         return t_detail[0] ? W8A8_ERR_CUDA : cuda_fail("attention launch", e);

@@ -2,20 +2,24 @@
 // O = softmax(scale Q K^T) V per sequence and head, causal or full, heads in
 // groups over the KV heads.
 //
-// A CTA owns two tiles of 128 packed rows of one KV head.  Row r of a
-// sequence is (query r / G, head r % G of the group), so a group's heads share
-// the keys that pass through shared memory, short sequences still fill tiles,
-// and a causal tile spans 128 / G positions.  Keys stream in tiles of 128.
-// For tile t and key tile j
+// An item is two tiles of 128 packed rows of one KV head.  Row r of a tile is
+// (query r / G, head r % G of the group), for the 128 / G queries that fit, so
+// a group's heads share the keys that pass through shared memory, short
+// sequences still fill tiles, and a causal tile spans few positions.  Keys
+// stream in tiles of 128.  For tile t and key tile j
 //   S = Q_t K_j^T        operands in shared memory, S (128 x 128, binary32) in TMEM
 //   P = 2^(scale log2(e) S - M), in the inputs' type, over S's own columns
 //   O_t += P V_j         P from TMEM, V_j (keys x D, D contiguous) as the
 //                        MN-major operand, O_t in TMEM
-// Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one thread per
-// row, which also loads Q and finishes O), warp 8 issues the MMAs, warp 9 the
-// TMA loads, warps 10-11 clean V (below).  While one tile's softmax runs, the
-// other tile's two products run: PV_0(j) S_0(j+1) PV_1(j) S_1(j+1).  MMAs of
-// one thread execute in order, so S_t(j+1) may overwrite P_t(j), and the commit
+//
+// CTAs are persistent, one per SM: each takes items (the longest of a sequence
+// first) from a counter.  Warps 0-3 and 4-7 are the softmax of tile 0 and 1
+// (one thread per row, which also finishes O), warp 8 issues the MMAs, warp 9
+// finds items and issues the TMA loads of Q, K and V, warps 10-11 clean V
+// (below).  Loads and first products of the next item run while the softmax
+// warps finish the present one.  While one tile's softmax runs, the other
+// tile's two products run: PV_0(j) S_0(j+1) PV_1(j) S_1(j+1).  MMAs of one
+// thread execute in order, so S_t(j+1) may overwrite P_t(j), and the commit
 // after S_t(j+1) also says that O_t holds all products up to j.
 //
 // M is any reference near the row's maximum: softmax does not change with
@@ -43,9 +47,9 @@ namespace w8a8 {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kItemRows = 2 * kTileRows;
 constexpr int kKeyTile = 128;
 constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
 constexpr float kSlack = 8.0f;  // log2 of the weight that moves the reference
 constexpr int kChunkBytes = 128 * 128;  // 128 rows of 64 16-bit elements
 
@@ -56,20 +60,31 @@ struct PromptSmem {
     static constexpr int kStages = DP == 128 ? 5 : 8;
     static constexpr int kPipe = 2 * kTileBytes;
     static constexpr int kBars = kPipe + kStages * kTileBytes;
-    static constexpr int kTotal = kBars + 384 + 1024;  // and room to align to 1024
+    static constexpr int kTotal = kBars + 512;
+};
+
+// What the warps need of an item.
+struct Item {
+    int q0, n, k0, m;   // the sequence
+    int hk, token0;     // KV head, first query of tile 0
+    int tiles[2];       // key tiles of each tile's rows
+    int edge;           // key tiles from here on are not seen completely by every row
+    int bad;            // a non-finite V of the sequence was taken out
+    int any;            // 0: no more items
 };
 
 struct Bars {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     // the V tiles to be cleaned: issued (so that the stage's barrier is in this
     // load's phase, not an older one of the same parity) and done; a slot per V
     // in the ring, as the cleaners run up to three tiles ahead of the products
     uint64_t v_issued[4], v_clean[4];
+    uint64_t item_full[2], item_empty[2], done;
     uint32_t tmem;
-    int bad;
+    Item items[2];
 };
-static_assert(sizeof(Bars) <= 384, "barriers fit their room");
+static_assert(sizeof(Bars) <= 512, "barriers fit their room");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
                                             int32_t c2) {
@@ -80,19 +95,46 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap,
         : "memory");
 }
 
-// 128-byte-swizzled operand whose M/N elements are contiguous (V as the
-// second product's B: N = D): 64 elements per 128-byte row, rows are keys.
-// Leading byte offset: from one 64-wide column block to the next; stride byte
-// offset: from 8 keys to the next 8.
-__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t smem_addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(kChunkBytes >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
+// Shared-memory operand descriptors with the 128-byte swizzle, low words built
+// from an address by adding (address >> 4); the high word is the same for all:
+// 1024 bytes between groups of 8 rows, descriptor version 1, swizzle type 2.
+// K-major (Q and K): rows of 64 elements of D, the leading offset is unused.
+// MN-major (V as the second product's B, N = D): 64 elements of D per 128-byte
+// row, rows are keys; leading offset from one 64-wide column block to the next.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescKMajor = 1u << 16;
+constexpr uint32_t kDescMnMajor = static_cast<uint32_t>(kChunkBytes >> 4) << 16;
+
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
 }
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// A place in the ring of S stages and the parity of its present round.
+template <int S>
+struct Ring {
+    int st = 0, ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == S) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
 
 template <typename T>
 constexpr uint32_t prompt_idesc(uint32_t n, bool b_mn_major) {
@@ -106,95 +148,83 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Byte offset of 16-byte chunk ch of row r in a tile as TMA writes it.
-__device__ __forceinline__ uint32_t tile_at(int r, int ch) {
-    return static_cast<uint32_t>((ch >> 3) * kChunkBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-}
-
-// The item of this CTA: rows [row0, row0 + 256) of KV head hk of sequence s.
-// A sequence's items run from its last rows (the most keys) to its first.
-struct Item {
-    bool any;
-    Sequence s;
-    int hk, row0;
-};
-
-__device__ __forceinline__ Item find_item(const AttentionArgs& p, int index) {
+// Item `index`, by one warp.  A sequence's items run from its last rows (the
+// most keys) to its first, KV heads innermost.
+__device__ __forceinline__ Item find_item(const AttentionArgs& p, int index, int tile_tokens) {
     const int lane = threadIdx.x & 31;
     Item it{};
-    int64_t before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        int64_t mine = 0;
-        if (b0 + lane < p.batch) {
-            const Sequence s = sequence(p, b0 + lane);
-            mine = (static_cast<int64_t>(s.n) * p.group + kItemRows - 1) / kItemRows * p.Hk;
-        }
-        int64_t incl = mine;
+        int mine = 0;
+        if (b0 + lane < p.batch) mine = (sequence(p, b0 + lane).n + 2 * tile_tokens - 1) / (2 * tile_tokens) * p.Hk;
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += t;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > index);
+        const unsigned hit = __ballot_sync(0xffffffffu, incl > index);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int local = static_cast<int>(index - (before + __shfl_sync(0xffffffffu, incl - mine, l)));
-            const int blocks = static_cast<int>(__shfl_sync(0xffffffffu, mine, l)) / p.Hk;
-            it.any = true;
-            it.s = sequence(p, b0 + l);
+            const int local = index - __shfl_sync(0xffffffffu, incl - mine, l);
+            const int blocks = __shfl_sync(0xffffffffu, mine, l) / p.Hk;
+            const Sequence s = sequence(p, b0 + l);
+            it.any = 1;
+            it.q0 = s.q0;
+            it.n = s.n;
+            it.k0 = s.k0;
+            it.m = s.m;
             it.hk = local % p.Hk;
-            it.row0 = (blocks - 1 - local / p.Hk) * kItemRows;
+            it.token0 = (blocks - 1 - local / p.Hk) * 2 * tile_tokens;
+            auto limit = [&](int token) { return p.causal ? clampi(token + s.m - s.n + 1, 0, s.m) : s.m; };
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int first = it.token0 + t * tile_tokens;
+                const int last = min(first + tile_tokens, s.n) - 1;
+                it.tiles[t] = first <= last ? (limit(last) + kKeyTile - 1) / kKeyTile : 0;
+            }
+            it.edge = limit(it.token0) / kKeyTile;
             return it;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        index -= __shfl_sync(0xffffffffu, incl, 31);
     }
     return it;
 }
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                            const AttentionArgs p) {
-    extern __shared__ uint8_t raw[];
+    attention_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ CUtensorMap tmV, const AttentionArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     using L = PromptSmem<DP>;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    constexpr int S = L::kStages;
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    const Item it = find_item(p, blockIdx.x);
-    if (!it.any) return;  // the whole CTA
-    const Sequence s = it.s;
-    const int rows_end = s.n * p.group;  // packed rows of the sequence
-    auto limit = [&](int pr) {  // keys that packed row pr sees: [0, limit)
-        return p.causal ? clampi(pr / p.group + s.m - s.n + 1, 0, s.m) : s.m;
-    };
-    int tiles[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = it.row0 + t * kTileRows;
-        const int last = min(first + kTileRows, rows_end) - 1;
-        tiles[t] = first <= last ? (limit(last) + kKeyTile - 1) / kKeyTile : 0;
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles start at multiples of 1024
+        if (threadIdx.x == 0) record_device_error(1);
+        return;
     }
-    const int jmax = max(tiles[0], tiles[1]);
-    const int edge = limit(it.row0) / kKeyTile;  // key tiles from here on are not seen completely by every row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile_tokens = kTileRows / p.group;
 
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
         if (lane == 0) {
-            for (int i = 0; i < L::kStages; ++i) {
+            for (int i = 0; i < S; ++i) {
                 mbar_init(&bars->kv_full[i], 1);
                 mbar_init(&bars->kv_empty[i], 1);
             }
             for (int t = 0; t < 2; ++t) {
-                mbar_init(&bars->q_full[t], 4);
+                mbar_init(&bars->q_full[t], 1);
+                mbar_init(&bars->q_empty[t], 1);
                 mbar_init(&bars->s_full[t], 1);
-                mbar_init(&bars->p_full[t], 4);
+                mbar_init(&bars->p_full[t], kSoftmaxWarps / 2);
                 mbar_init(&bars->o_full[t], 1);
+                mbar_init(&bars->item_full[t], 1);
+                mbar_init(&bars->item_empty[t], kSoftmaxWarps + 3);  // and MMA, 2 cleaners
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&bars->v_issued[i], 1);
                 mbar_init(&bars->v_clean[i], 2);
             }
-            bars->bad = 0;
+            mbar_init(&bars->done, 1);
             fence_mbarrier_init();
         }
         __syncwarp();
@@ -207,290 +237,378 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = bars->tmem;
     const uint32_t pipe = smem_u32(smem) + L::kPipe;
 
-    if (warp >= 8) {
+    auto leave_item = [&](int at) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[at & 1]);
+    };
+
+    if (warp >= kSoftmaxWarps) {
         regs_dec<72>();
-        if (warp == 9) {
-            // ---- TMA producer: K_0 V_0 K_1 V_1 ...
+        if (warp == kSoftmaxWarps + 1) {
+            // ---- items and TMA loads: K_0 Q_0 Q_1 V_0 K_1 V_1 ...
             if (elect_one_sync()) {
+                tma_prefetch_desc(&tmQ);
                 tma_prefetch_desc(&tmK);
                 tma_prefetch_desc(&tmV);
-                int ld = 0;
-                for (; ld < 2 * jmax; ++ld) {
-                    const int st = ld % L::kStages;
-                    if (ld >= L::kStages && !mbar_wait(&bars->kv_empty[st], (ld / L::kStages - 1) & 1, 60)) break;
-                    mbar_arrive_expect_tx(&bars->kv_full[st], L::kTileBytes);
-                    const void* map = (ld & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
-#pragma unroll
-                    for (int c = 0; c < L::kChunks; ++c)
-                        tma_load_3d(pipe + st * L::kTileBytes + c * kChunkBytes, map, &bars->kv_full[st], 64 * c,
-                                    it.hk, s.k0 + (ld >> 1) * kKeyTile);
-                    if ((ld & 1) && (ld >> 1) >= edge) mbar_arrive(&bars->v_issued[((ld >> 1) - edge) & 3]);
-                }
-                // nothing is in flight into this CTA's shared memory when it ends
-                for (int i = max(0, ld - L::kStages); i < ld; ++i)
-                    mbar_wait(&bars->kv_full[i % L::kStages], (i / L::kStages) & 1, 60);
             }
-        } else if (warp == 8) {
-            // ---- MMA issuer
-            const bool leader = elect_one_sync();
-            auto scores = [&](int t, int ld) {
-                if (!leader) return;
-                const uint32_t a = smem_u32(smem) + t * L::kTileBytes;
-                const uint32_t b = pipe + (ld % L::kStages) * L::kTileBytes;
+            const uint32_t q_bytes = L::kChunks * tile_tokens * p.group * 128;
+            int index = blockIdx.x, edges = 0;
+            int q_ph[2] = {1, 1};  // a fresh barrier lets the first wait through
+            Ring<S> r;
+            r.ph = 1;
+            bool ok = true;
+            for (int at = 0; ok; ++at) {
+                Item it = find_item(p, index, tile_tokens);
+                if (!mbar_wait(&bars->item_empty[at & 1], ((at >> 1) & 1) ^ 1, 60)) {
+                    it.any = 0;
+                    ok = false;
+                }
+                if (lane == 0) {
+                    bars->items[at & 1] = it;
+                    mbar_arrive(&bars->item_full[at & 1]);
+                }
+                if (!it.any) break;
+                if (lane == 0) index = atomicAdd(p.counters, 1);
+                const int jmax = max(it.tiles[0], it.tiles[1]);
+                for (int i = 0; i < 2 * jmax; ++i) {
+                    const int j = i >> 1;
+                    ok = mbar_wait(&bars->kv_empty[r.st], r.ph, 61);
+                    if (!ok) break;
+                    if (elect_one_sync()) {
+                        mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
+                        const void* map = (i & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+#pragma unroll
+                        for (int c = 0; c < L::kChunks; ++c)
+                            tma_load_3d(pipe + r.st * L::kTileBytes + c * kChunkBytes, map, &bars->kv_full[r.st],
+                                        64 * c, it.hk, it.k0 + j * kKeyTile);
+                        if ((i & 1) && j >= it.edge) mbar_arrive(&bars->v_issued[(edges + j - it.edge) & 3]);
+                    }
+                    r.next();
+                    if (i == 0) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (it.tiles[t] == 0) continue;
+                            ok = ok && mbar_wait(&bars->q_empty[t], q_ph[t], 62);
+                            q_ph[t] ^= 1;
+                            if (ok && elect_one_sync()) {
+                                mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
+#pragma unroll
+                                for (int c = 0; c < L::kChunks; ++c)
+                                    tma_load_3d(smem_u32(smem) + t * L::kTileBytes + c * kChunkBytes, &tmQ,
+                                                &bars->q_full[t], 64 * c, it.hk * p.group,
+                                                it.q0 + it.token0 + t * tile_tokens);
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                }
+                edges += max(0, jmax - it.edge);
+                index = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, index, 0);
+            }
+            // nothing is in flight into this CTA's shared memory when it ends
+            // (a stage's last load is complete when its barrier has left that round;
+            // a stage never loaded has parity 1 behind it)
+            for (int i = 0; i < S; ++i) {
+                mbar_wait(&bars->kv_full[r.st], r.ph, 61);
+                r.next();
+            }
+            for (int t = 0; t < 2; ++t) mbar_wait(&bars->q_full[t], q_ph[t], 62);
+            // the last CTA to run out of items leaves the counters at zero
+            if (lane == 0) {
+                __threadfence();
+                if (atomicAdd(p.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+                    p.counters[0] = 0;
+                    p.counters[1] = 0;
+                }
+            }
+        } else if (warp == kSoftmaxWarps) {
+            // ---- MMA issuer, one thread throughout (so that the MMAs' operands are uniform)
+            if (elect_one_sync()) {
+            const uint32_t q_low = (smem_u32(smem) >> 4) | kDescKMajor, kv_low = pipe >> 4;
+            constexpr int kTileLow = L::kTileBytes >> 4;
+            auto scores = [&](int t, int st) {
+                const uint32_t a = q_low + t * kTileLow, b = (kv_low + st * kTileLow) | kDescKMajor;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t at = (k >> 2) * kChunkBytes + (k & 3) * 32;
-                    mma_bf16_ss(tmem + t * 128, smem_desc_kmajor_sw128(a + at), smem_desc_kmajor_sw128(b + at),
-                                prompt_idesc<T>(kKeyTile, false), k > 0);
+                    const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4;
+                    mma_scores(tmem + t * 128, a + off, b + off, prompt_idesc<T>(kKeyTile, false), k > 0);
                 }
                 mma_commit(&bars->s_full[t]);
             };
-            bool ok = jmax > 0 && mbar_wait(&bars->kv_full[0], 0, 61);
-            for (int t = 0; t < 2 && ok; ++t)
-                if (tiles[t] > 0) {
-                    ok = mbar_wait(&bars->q_full[t], 0, 62);
-                    tc_fence_after();
-                    if (ok) scores(t, 0);
-                }
-            // a stage is released only to a load that will come
-            if (ok && leader && L::kStages < 2 * jmax) mma_commit(&bars->kv_empty[0]);
-            for (int j = 0; j < jmax && ok; ++j) {
-                const int lv = 2 * j + 1, lk = 2 * j + 2;
-                ok = mbar_wait(&bars->kv_full[lv % L::kStages], (lv / L::kStages) & 1, 63);
-                if (ok && j >= edge) ok = mbar_wait(&bars->v_clean[(j - edge) & 3], ((j - edge) >> 2) & 1, 64);
-                if (ok && j + 1 < jmax) ok = mbar_wait(&bars->kv_full[lk % L::kStages], (lk / L::kStages) & 1, 65);
+            int edges = 0, q_ph = 0, p_ph = 0;  // bit t: tile t's parity
+            Ring<S> r;
+            bool ok = true;
+            for (int at = 0; ok; ++at) {
+                if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 63)) break;
+                const volatile Item& it = bars->items[at & 1];
+                const int any = it.any, tiles0 = it.tiles[0], tiles1 = it.tiles[1], edge = it.edge;
+                if (!any) break;
+                mbar_arrive(&bars->item_empty[at & 1]);
+                const int jmax = max(tiles0, tiles1);
+                if (jmax == 0) continue;
+                ok = mbar_wait(&bars->kv_full[r.st], r.ph, 64);
                 for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= tiles[t]) continue;
-                    ok = mbar_wait(&bars->p_full[t], j & 1, 66);
-                    if (!ok) break;
+                    const int tiles = t ? tiles1 : tiles0;
+                    if (tiles == 0) continue;
+                    ok = mbar_wait(&bars->q_full[t], (q_ph >> t) & 1, 65);
+                    q_ph ^= 1 << t;
                     tc_fence_after();
-                    if (leader) {
-                        const uint32_t b = pipe + (lv % L::kStages) * L::kTileBytes;
+                    if (ok) {
+                        scores(t, r.st);
+                        if (tiles == 1) mma_commit(&bars->q_empty[t]);
+                    }
+                }
+                if (ok) mma_commit(&bars->kv_empty[r.st]);
+                r.next();
+                for (int j = 0; j < jmax && ok; ++j) {
+                    const int vst = r.st;
+                    ok = mbar_wait(&bars->kv_full[r.st], r.ph, 66);
+                    r.next();
+                    if (ok && j >= edge) {
+                        ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67);
+                        ++edges;
+                    }
+                    const int kst = r.st;
+                    if (j + 1 < jmax) {
+                        ok = ok && mbar_wait(&bars->kv_full[r.st], r.ph, 68);
+                        r.next();
+                    }
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const int tiles = t ? tiles1 : tiles0;
+                        if (j >= tiles) continue;
+                        ok = mbar_wait(&bars->p_full[t], (p_ph >> t) & 1, 69);
+                        p_ph ^= 1 << t;
+                        tc_fence_after();
+                        if (!ok) break;
+                        const uint32_t b = (kv_low + vst * kTileLow) | kDescMnMajor;
 #pragma unroll
                         for (int k = 0; k < kKeyTile / 16; ++k)
-                            mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                                       smem_desc_mnmajor_sw128(b + k * 2048), prompt_idesc<T>(DP, true), j + k > 0);
+                            mma_output(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                                       b + k * (2048 >> 4), prompt_idesc<T>(DP, true), j + k > 0);
+                        if (j + 1 < tiles) {
+                            scores(t, kst);
+                            if (j + 2 == tiles) mma_commit(&bars->q_empty[t]);
+                        } else {
+                            mma_commit(&bars->o_full[t]);
+                        }
                     }
-                    if (j + 1 < tiles[t]) scores(t, lk);
-                    else if (leader) mma_commit(&bars->o_full[t]);
-                }
-                if (ok && leader) {
-                    if (lv + L::kStages < 2 * jmax) mma_commit(&bars->kv_empty[lv % L::kStages]);
-                    if (lk + L::kStages < 2 * jmax) mma_commit(&bars->kv_empty[lk % L::kStages]);
+                    if (ok) {
+                        mma_commit(&bars->kv_empty[vst]);
+                        if (j + 1 < jmax) mma_commit(&bars->kv_empty[kst]);
+                    }
                 }
             }
+            // every commit has arrived before the CTA ends
+            mma_commit(&bars->done);
+            mbar_wait(&bars->done, 0, 70);
+            }
+            __syncwarp();
         } else {
             // ---- V cleaners: key tiles from `edge` on
-            const int me = threadIdx.x - 320;  // 0..63
+            const int me = threadIdx.x - 32 * (kSoftmaxWarps + 2);  // 0..63
+            int ld = 0, edges = 0;
             bool ok = true;
-            for (int j = edge; j < jmax && ok; ++j) {
-                const int lv = 2 * j + 1;
-                ok = mbar_wait(&bars->v_issued[(j - edge) & 3], ((j - edge) >> 2) & 1, 67) &&
-                     mbar_wait(&bars->kv_full[lv % L::kStages], (lv / L::kStages) & 1, 67);
-                if (!ok) break;
-                const uint32_t v = pipe + (lv % L::kStages) * L::kTileBytes;
+            for (int at = 0; ok; ++at) {
+                if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 71)) break;
+                volatile Item& it = bars->items[at & 1];
+                if (!it.any) break;
+                const int jmax = max(it.tiles[0], it.tiles[1]);
+                for (int j = it.edge; j < jmax && ok; ++j, ++edges) {
+                    const int lv = ld + 2 * j + 1;
+                    ok = mbar_wait(&bars->v_issued[edges & 3], (edges >> 2) & 1, 72) &&
+                         mbar_wait(&bars->kv_full[lv % S], (lv / S) & 1, 73);
+                    if (!ok) break;
+                    const uint32_t v = pipe + (lv % S) * L::kTileBytes;
 #pragma unroll 4
-                for (int c = me; c < L::kTileBytes / 16; c += 64) {
-                    uint4 w;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                 : "r"(v + 16 * c));
-                    if (any_non_finite<T>(w)) {
-                        constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    for (int c = me; c < L::kTileBytes / 16; c += 64) {
+                        uint4 w;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(v + 16 * c));
+                        if (any_non_finite<T>(w)) {
+                            constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+                            uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((u[i] & e) == e) u[i] &= 0xFFFF0000u;
-                            if (((u[i] >> 16) & e) == e) u[i] &= 0x0000FFFFu;
+                            for (int i = 0; i < 4; ++i) {
+                                if ((u[i] & e) == e) u[i] &= 0xFFFF0000u;
+                                if (((u[i] >> 16) & e) == e) u[i] &= 0x0000FFFFu;
+                            }
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v + 16 * c), "r"(u[0]),
+                                         "r"(u[1]), "r"(u[2]), "r"(u[3])
+                                         : "memory");
+                            const int key = j * kKeyTile + ((c >> 3) & 127);
+                            if (key < it.m) it.bad = 1;
                         }
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v + 16 * c), "r"(u[0]),
-                                     "r"(u[1]), "r"(u[2]), "r"(u[3])
-                                     : "memory");
-                        const int key = j * kKeyTile + ((c >> 3) & 127);
-                        if (key < s.m) *reinterpret_cast<volatile int*>(&bars->bad) = 1;
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->v_clean[edges & 3]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->v_clean[(j - edge) & 3]);
+                ld += 2 * jmax;
+                leave_item(at);
             }
         }
     } else {
         // ---- softmax, one thread per row
         regs_inc<208>();
         const int t = warp >> 2, wq = warp & 3;
-        const int pr = it.row0 + t * kTileRows + wq * 32 + lane;
-        const bool valid = pr < rows_end;
-        const int query = pr / p.group, head = it.hk * p.group + (pr - query * p.group);
-        const int lim = valid ? limit(pr) : 0;
-        const int warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : s.m);
-        const uint32_t qtile = smem_u32(smem) + t * L::kTileBytes;
+        const int row = wq * 32 + lane;
+        const int row_token = t * tile_tokens + row / p.group, row_head = row % p.group;
+        const bool used = row < tile_tokens * p.group;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-        constexpr int kRowChunks = DP / 8, kRowsAtOnce = 32 / kRowChunks;
-        const int sub = lane / kRowChunks, ch = lane % kRowChunks;
-
-        {  // Q rows of this warp
-            const int64_t at = static_cast<int64_t>(s.q0 + query) * p.q_token + static_cast<int64_t>(head) * p.q_head;
-#pragma unroll 8
-            for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
-                const int r = r0 + sub;
-                const int64_t src = __shfl_sync(0xffffffffu, at, r);
-                const bool take = __shfl_sync(0xffffffffu, valid, r) && 8 * ch < p.D;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (take) w = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + src + 8 * ch);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qtile + tile_at(wq * 32 + r, ch)),
-                             "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->q_full[t]);
-        }
-
         const float c = p.scale_log2;
         const uint64_t c2 = f2_pack(c, c);
-        float ref = -INFINITY;
-        uint64_t sum2 = f2_pack(0.0f, 0.0f);
+        int s_ph = 0, o_ph = 0;
         bool ok = true;
-        for (int j = 0; j < tiles[t]; ++j) {
-            ok = mbar_wait(&bars->s_full[t], j & 1, 68);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t v[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_wait_ld_regs32(v[i]);
-            const int left = lim - j * kKeyTile;  // columns this row sees
-            if (warp_lim < (j + 1) * kKeyTile) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (32 * i + x >= left) v[i][x] = 0xFF800000u;  // -inf
+        for (int at = 0; ok; ++at) {
+            if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 74)) break;
+            const volatile Item& it = bars->items[at & 1];
+            if (!it.any) break;
+            int lim, warp_lim;
+            {
+                const int n = it.n, m = it.m, token = it.token0 + row_token;
+                const bool valid = used && token < n;
+                lim = valid ? (p.causal ? clampi(token + m - n + 1, 0, m) : m) : 0;
+                warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : m);
             }
-            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+            const int tiles = it.tiles[t];
+            float ref = -INFINITY;
+            uint64_t sum2 = f2_pack(0.0f, 0.0f);
+            for (int j = 0; j < tiles; ++j) {
+                ok = mbar_wait(&bars->s_full[t], s_ph, 75);
+                if (!ok) break;
+                s_ph ^= 1;
+                tc_fence_after();
+                uint32_t v[4][32];
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                m0 = max3(m0, __uint_as_float(v[0][x]), __uint_as_float(v[0][x + 1]));
-                m1 = max3(m1, __uint_as_float(v[1][x]), __uint_as_float(v[1][x + 1]));
-                m2 = max3(m2, __uint_as_float(v[2][x]), __uint_as_float(v[2][x + 1]));
-                m3 = max3(m3, __uint_as_float(v[3][x]), __uint_as_float(v[3][x + 1]));
-            }
-            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * c;
-            if (j == 0) {
-                ref = top;
-            } else {
-                const bool moves = top > ref + kSlack;  // also from -inf
-                if (__any_sync(0xffffffffu, moves)) {
-                    const float f = moves ? exp2_approx(ref - top) : 1.0f;
-                    if (moves) ref = top;
-                    const uint64_t f2 = f2_pack(f, f);
-                    sum2 = f2_mul(sum2, f2);
+                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_wait_ld_regs32(v[i]);
+                if (warp_lim < (j + 1) * kKeyTile) {
+                    const int left = lim - j * kKeyTile;  // columns this row sees
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * i + k >= left) v[i][k] = 0xFF800000u;  // -inf
+                }
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m[i] = max3(m[i], __uint_as_float(v[i][k]), __uint_as_float(v[i][k + 1]));
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
+                if (j == 0) {
+                    ref = top;
+                } else {
+                    const bool moves = top > ref + kSlack;  // also from -inf
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float f = moves ? exp2_approx(ref - top) : 1.0f;
+                        if (moves) ref = top;
+                        sum2 = f2_mul(sum2, f2_pack(f, f));
 #pragma unroll 1
-                    for (int i = 0; i < DP / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(to + 16 * i, o);
-                        tmem_wait_ld_regs(o);
+                        for (int i = 0; i < DP / 16; ++i) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(to + 16 * i, o);
+                            tmem_wait_ld_regs(o);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tmem_st_32x32b_x16(to + 16 * i, o);
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st_32x32b_x16(to + 16 * i, o);
+                        }
                     }
                 }
-            }
-            const float base = ref == -INFINITY ? 0.0f : -ref;
-            const uint64_t base2 = f2_pack(base, base);
+                const float base = ref == -INFINITY ? 0.0f : -ref;
+                const uint64_t base2 = f2_pack(base, base);
+                uint64_t part2[2] = {sum2, f2_pack(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[16];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    float a, b;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i][x]), __uint_as_float(v[i][x + 1])), c2, base2), a, b);
-                    a = exp2_approx(a);
-                    b = exp2_approx(b);
-                    sum2 = f2_add(sum2, f2_pack(a, b));
-                    w[x >> 1] = Pair16<T>::pack(a, b);
+                    for (int k = 0; k < 32; k += 2) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i][k]), __uint_as_float(v[i][k + 1])), c2, base2), a,
+                                  b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        part2[(k >> 1) & 1] = f2_add(part2[(k >> 1) & 1], f2_pack(a, b));
+                        w[k >> 1] = Pair16<T>::pack(a, b);
+                    }
+                    tmem_st_32x32b_x16(ts + 16 * i, w);
                 }
-                tmem_st_32x32b_x16(ts + 16 * i, w);
+                sum2 = f2_add(part2[0], part2[1]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[t]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[t]);
-        }
 
-        // ---- O / sum, through this warp's rows of the Q tile, to memory
-        float l0, l1;
-        f2_unpack(sum2, l0, l1);
-        const float l = l0 + l1;
-        if (tiles[t] > 0 && ok) ok = mbar_wait(&bars->o_full[t], 0, 69);
-        tc_fence_after();
-        const int bad = tiles[t] > 0 ? *reinterpret_cast<volatile int*>(&bars->bad) : 0;
-        const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
-        if (ok) {
+            // ---- O / sum to memory
+            float l0, l1;
+            f2_unpack(sum2, l0, l1);
+            const float l = l0 + l1;
+            if (tiles > 0) {
+                ok = ok && mbar_wait(&bars->o_full[t], o_ph, 76);
+                o_ph ^= 1;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const int bad = tiles > 0 ? it.bad : 0;
+            const int q0 = it.q0, k0 = it.k0, hk = it.hk, token = it.token0 + row_token, edge = it.edge;
+            const bool valid = used && token < it.n;
+            leave_item(at);
+            const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
+            const int head = hk * p.group + row_head;
+            T* dst = static_cast<T*>(p.o) + static_cast<int64_t>(q0 + token) * p.o_token +
+                     static_cast<int64_t>(head) * p.o_head;
 #pragma unroll 1
-            for (int i = 0; i < DP / 16; ++i) {
-                uint32_t o[16];
-                if (tiles[t] > 0) {
-                    tmem_ld_32x32b_x16(to + 16 * i, o);
-                    tmem_wait_ld_regs(o);
+            for (int i = 0; i < DP / 32; ++i) {
+                uint32_t o[32];
+                const int col = 32 * i;
+                if (tiles > 0) {
+                    tmem_ld_32x32b_x32(to + 32 * i, o);
+                    tmem_wait_ld_regs32(o);
                 }
                 if (bad) {
                     for (int key = edge * kKeyTile; key < lim; ++key) {
-                        const T* src = static_cast<const T*>(p.v) + static_cast<int64_t>(s.k0 + key) * p.v_token +
-                                       static_cast<int64_t>(it.hk) * p.v_head + 16 * i;
+                        const T* src = static_cast<const T*>(p.v) + static_cast<int64_t>(k0 + key) * p.v_token +
+                                       static_cast<int64_t>(hk) * p.v_head + col;
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            if (16 * i + x >= p.D) continue;
+                        for (int x = 0; x < 32; ++x) {
+                            if (col + x >= p.D) continue;
                             const float val = static_cast<float>(src[x]);
                             if (!isfinite(val)) o[x] = __float_as_uint(__uint_as_float(o[x]) + val);
                         }
                     }
                 }
-                uint32_t w[8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    w[x] = lim > 0 ? Pair16<T>::pack(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv)
-                                   : 0u;
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     qtile + tile_at(wq * 32 + lane, 2 * i + h)),
-                                 "r"(w[4 * h]), "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
-                                 : "memory");
-            }
-            __syncwarp();
-            const int64_t at = static_cast<int64_t>(s.q0 + query) * p.o_token + static_cast<int64_t>(head) * p.o_head;
-#pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
-                const int r = r0 + sub;
-                const int64_t dst = __shfl_sync(0xffffffffu, at, r);
-                const bool take = __shfl_sync(0xffffffffu, valid, r) && 8 * ch < p.D;
-                uint4 w;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                             : "r"(qtile + tile_at(wq * 32 + r, ch))
-                             : "memory");
-                if (take) *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + dst + 8 * ch) = w;
+                    for (int x = 0; x < 4; ++x)
+                        w[x] = lim > 0 ? Pair16<T>::pack(__uint_as_float(o[8 * h + 2 * x]) * inv,
+                                                         __uint_as_float(o[8 * h + 2 * x + 1]) * inv)
+                                       : 0u;
+                    if (valid && col + 8 * h < p.D)
+                        *reinterpret_cast<uint4*>(dst + col + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
             if (p.lse && valid)
-                p.lse[static_cast<int64_t>(s.q0 + query) * p.Hq + head] =
+                p.lse[static_cast<int64_t>(q0 + token) * p.Hq + head] =
                     lim > 0 ? ((ref == -INFINITY ? 0.0f : ref) + log2f(l)) * kLn2 : -INFINITY;
+            tc_fence_before();
         }
-        tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
 template <typename T, int DP>
-cudaError_t launch_prompt_typed(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttentionArgs& a, int grid,
-                                cudaStream_t st) {
+cudaError_t launch_prompt_typed(const CUtensorMap (&map)[3], const AttentionArgs& a, int grid, cudaStream_t st) {
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -501,50 +619,60 @@ cudaError_t launch_prompt_typed(const CUtensorMap& tmK, const CUtensorMap& tmV, 
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
-    attention_prompt_kernel<T, DP><<<grid, kThreads, PromptSmem<DP>::kTotal, st>>>(tmK, tmV, a);
+    attention_prompt_kernel<T, DP><<<grid, kThreads, PromptSmem<DP>::kTotal, st>>>(map[0], map[1], map[2], a);
     return cudaGetLastError();
+}
+
+// An upper bound on the items of any split of the rows into sequences.
+int64_t most_items(const AttentionArgs& a) {
+    return (static_cast<int64_t>(a.Tq) / (2 * (kTileRows / a.group)) + a.batch) * a.Hk;
 }
 
 }  // namespace
 
 bool attention_prompt_takes(const AttentionArgs& a) {
     // TMA strides are positive and below 2^40 bytes
-    const int64_t s[4] = {a.k_token, a.k_head, a.v_token, a.v_head};
+    const int64_t s[6] = {a.q_token, a.q_head, a.k_token, a.k_head, a.v_token, a.v_head};
     for (int64_t v : s)
         if (v <= 0 || v >= int64_t(1) << 39) return false;
-    const int64_t items = (static_cast<int64_t>(a.Tq) * a.group / kItemRows + a.batch) * a.Hk;
-    return a.Tk > 0 && items <= INT32_MAX && static_cast<int64_t>(a.Tq) * a.group <= INT32_MAX;
+    return a.Tk > 0 && a.group <= kTileRows && most_items(a) <= INT32_MAX / 2;
 }
 
-cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, void* encode_fn, cudaStream_t st, char* detail,
-                                    size_t n) {
+cudaError_t launch_attention_prompt(const AttentionArgs& args, int dtype, int num_sms, void* workspace,
+                                    void* encode_fn, cudaStream_t st, char* detail, size_t n) {
+    AttentionArgs a = args;
+    a.counters = static_cast<int*>(workspace);
     auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode_fn);
-    CUtensorMap map[2];
-    for (int i = 0; i < 2; ++i) {
-        const void* ptr = i ? a.v : a.k;
-        const int64_t token = i ? a.v_token : a.k_token, head = i ? a.v_head : a.k_head;
-        cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.Hk),
-                              static_cast<cuuint64_t>(a.Tk)};
+    CUtensorMap map[3];
+    for (int i = 0; i < 3; ++i) {
+        const void* ptr = i == 0 ? a.q : i == 1 ? a.k : a.v;
+        const int64_t token = i == 0 ? a.q_token : i == 1 ? a.k_token : a.v_token;
+        const int64_t head = i == 0 ? a.q_head : i == 1 ? a.k_head : a.v_head;
+        const int heads = i == 0 ? a.Hq : a.Hk, rows = i == 0 ? a.Tq : a.Tk;
+        cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
         cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2};
-        cuuint32_t box[3] = {64, 1, kKeyTile};
+        cuuint32_t box[3] = {64, i == 0 ? static_cast<cuuint32_t>(a.group) : 1u,
+                             i == 0 ? static_cast<cuuint32_t>(kTileRows / a.group) : static_cast<cuuint32_t>(kKeyTile)};
         cuuint32_t estr[3] = {1, 1, 1};
-        const CUresult r = encode(&map[i], dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                                  3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        const CUresult r = encode(&map[i],
+                                  dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) {
-            snprintf(detail, n, "cuTensorMapEncodeTiled(%s: %d x %d x %d) returned %d", i ? "V" : "K", a.Tk, a.Hk, a.D,
+            snprintf(detail, n, "cuTensorMapEncodeTiled(%c: %d x %d x %d) returned %d", "QKV"[i], rows, heads, a.D,
                      static_cast<int>(r));
             return cudaErrorInvalidValue;
         }
     }
-    // an upper bound on the items of any split of the rows into sequences
-    const int grid = static_cast<int>((static_cast<int64_t>(a.Tq) * a.group / kItemRows + a.batch) * a.Hk);
+    const int64_t items = most_items(a);
+    const int grid = items < num_sms ? static_cast<int>(items) : num_sms;
     if (dtype == kBf16)
-        return a.D <= 64 ? launch_prompt_typed<__nv_bfloat16, 64>(map[0], map[1], a, grid, st)
-                         : launch_prompt_typed<__nv_bfloat16, 128>(map[0], map[1], a, grid, st);
-    return a.D <= 64 ? launch_prompt_typed<__half, 64>(map[0], map[1], a, grid, st)
-                     : launch_prompt_typed<__half, 128>(map[0], map[1], a, grid, st);
+        return a.D <= 64 ? launch_prompt_typed<__nv_bfloat16, 64>(map, a, grid, st)
+                         : launch_prompt_typed<__nv_bfloat16, 128>(map, a, grid, st);
+    return a.D <= 64 ? launch_prompt_typed<__half, 64>(map, a, grid, st)
+                     : launch_prompt_typed<__half, 128>(map, a, grid, st);
 }
 
 cudaError_t attention_read_device_error(unsigned int* code) {

@@ -122,8 +122,8 @@ cudaError_t launch_attention(const AttentionArgs& a, int dtype, int num_sms, voi
 // takes; `encode_fn` is the driver's cuTensorMapEncodeTiled.  On failure a
 // one-line description is written to `detail` (size `n`).
 bool attention_prompt_takes(const AttentionArgs& a);
-cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, void* encode_fn, cudaStream_t st, char* detail,
-                                    size_t n);
+cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, int num_sms, void* workspace, void* encode_fn,
+                                    cudaStream_t st, char* detail, size_t n);
 cudaError_t attention_read_device_error(unsigned int* code);
 
 // One [rows, heads, dim] side of the rotary kernel; strides count elements.
