@@ -26,7 +26,8 @@
 // it.  It moves only when a score exceeds it by more than 2^8 in weight; only
 // then is O_t rescaled (by the softmax threads, between products).  Sums and O
 // stay binary32; P's rounding to 16 bits is half a step of each weight, as in
-// the output.
+// the output.  The two halves of P go to the second product one after the
+// other.
 //
 // A weight of 0 does not hide a non-finite V (0 * inf = NaN).  In the key tiles
 // that some row does not see completely, warps 10-11 therefore replace the
@@ -75,7 +76,7 @@ struct Item {
 
 struct Bars {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
     // the V tiles to be cleaned: issued (so that the stage's barrier is in this
     // load's phase, not an older one of the same parity) and done; a slot per V
     // in the ring, as the cleaners run up to three tiles ahead of the products
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->q_full[t], 1);
                 mbar_init(&bars->q_empty[t], 1);
                 mbar_init(&bars->s_full[t], 1);
-                mbar_init(&bars->p_full[t], kSoftmaxWarps / 2);
+                mbar_init(&bars->p_full[t][0], kSoftmaxWarps / 2);
+                mbar_init(&bars->p_full[t][1], kSoftmaxWarps / 2);
                 mbar_init(&bars->o_full[t], 1);
                 mbar_init(&bars->item_full[t], 1);
                 mbar_init(&bars->item_empty[t], kSoftmaxWarps + 3);  // and MMA, 2 cleaners
@@ -376,15 +378,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < 2 && ok; ++t) {
                         const int tiles = t ? tiles1 : tiles0;
                         if (j >= tiles) continue;
-                        ok = mbar_wait(&bars->p_full[t], (p_ph >> t) & 1, 69);
-                        p_ph ^= 1 << t;
-                        tc_fence_after();
-                        if (!ok) break;
                         const uint32_t b = (kv_low + vst * kTileLow) | kDescMnMajor;
 #pragma unroll
-                        for (int k = 0; k < kKeyTile / 16; ++k)
-                            mma_output(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                                       b + k * (2048 >> 4), prompt_idesc<T>(DP, true), j + k > 0);
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && mbar_wait(&bars->p_full[t][half], (p_ph >> t) & 1, 69);
+                            tc_fence_after();
+                            if (!ok) break;
+#pragma unroll
+                            for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                mma_output(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, b + k * (2048 >> 4),
+                                           prompt_idesc<T>(DP, true), j + k > 0);
+                        }
+                        if (!ok) break;
+                        p_ph ^= 1 << t;
                         if (j + 1 < tiles) {
                             scores(t, kst);
                             if (j + 2 == tiles) mma_commit(&bars->q_empty[t]);
@@ -536,12 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[k >> 1] = Pair16<T>::pack(a, b);
                     }
                     tmem_st_32x32b_x16(ts + 16 * i, w);
+                    if (i & 1) {  // half of P: its product can start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->p_full[t][i >> 1]);
+                    }
                 }
                 sum2 = f2_add(part2[0], part2[1]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[t]);
             }
 
             // ---- O / sum to memory
