@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 
@@ -95,16 +96,13 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Whether any of the eight 16-bit floats in w is infinite or NaN (all
-// exponent bits set).
+// Whether any of the eight 16-bit floats in w is infinite or NaN: the
+// magnitude plus one in the exponent's last place carries into the sign bit.
 template <typename T>
 __device__ __forceinline__ bool any_non_finite(const uint4& w) {
-    const uint32_t e = sizeof(T) && (std::is_same<T, __half>::value) ? 0x7C00u : 0x7F80u;
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (u[i] & e) == e || ((u[i] >> 16) & e) == e;
-    return bad;
+    constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    const uint32_t m = 0x7FFF7FFFu;
+    return ((((w.x & m) + one) | ((w.y & m) + one) | ((w.z & m) + one) | ((w.w & m) + one)) & 0x80008000u) != 0;
 }
 
 }  // namespace

@@ -17,10 +17,16 @@
 // (one thread per row, which also finishes O), warp 8 issues the MMAs, warp 9
 // finds items and issues the TMA loads of Q, K and V, warps 10-11 clean V
 // (below).  Loads and first products of the next item run while the softmax
-// warps finish the present one.  While one tile's softmax runs, the other
-// tile's two products run: PV_0(j) S_0(j+1) PV_1(j) S_1(j+1).  MMAs of one
-// thread execute in order, so S_t(j+1) may overwrite P_t(j), and the commit
-// after S_t(j+1) also says that O_t holds all products up to j.
+// warps finish the present one.
+//
+// The tiles' steps alternate: step n of an item is (tile n mod T, key tile
+// n / T), T = 2, or 1 where the second tile has no rows.  S and P of a step lie
+// in one of B buffers in TMEM, in turn, and the MMA thread issues PV of step n
+// and then S of step n + B into the same buffer: MMAs of one thread execute in
+// order, so S may overwrite P.  O of both tiles takes 2 D of TMEM's 512 columns
+// and a buffer 128: B = 2 for D = 128 (while one tile's softmax runs, the other
+// tile's two products run) and 3 for D = 64 (a tile's next S is there before
+// its softmax ends).
 //
 // M is any reference near the row's maximum: softmax does not change with
 // it.  It moves only when a score exceeds it by more than 2^8 in weight; only
@@ -58,17 +64,22 @@ template <int DP>
 struct PromptSmem {
     static constexpr int kChunks = DP / 64;
     static constexpr int kTileBytes = kChunks * kChunkBytes;  // a Q, K or V tile
-    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kStages = DP == 128 ? 4 : 8;
     static constexpr int kPipe = 2 * kTileBytes;
-    static constexpr int kBars = kPipe + kStages * kTileBytes;
-    static constexpr int kTotal = kBars + 512;
+    static constexpr int kOut = kPipe + kStages * kTileBytes;  // 32 rows of 64 outputs for each softmax warp
+    static constexpr int kOutBytes = 32 * 128;
+    static constexpr int kBars = kOut + kSoftmaxWarps * kOutBytes;
+    static constexpr int kTotal = kBars + 768;
+    static constexpr int kBuffers = DP == 128 ? 2 : 3;  // of S and P in TMEM
+    static constexpr int kOutputs = 128 * kBuffers;     // TMEM column of tile 0's O
 };
 
 // What the warps need of an item.
 struct Item {
     int q0, n, k0, m;   // the sequence
     int hk, token0;     // KV head, first query of tile 0
-    int tiles[2];       // key tiles of each tile's rows
+    int tiles;          // tiles with rows: 1 or 2
+    int keys;           // key tiles that some row sees
     int edge;           // key tiles from here on are not seen completely by every row
     int bad;            // a non-finite V of the sequence was taken out
     int any;            // 0: no more items
@@ -76,7 +87,10 @@ struct Item {
 
 struct Bars {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
+    uint64_t q_full[2], q_empty[2];
+    // S and PV of a tile's own step k complete s_full and pv_done[tile][k mod 4];
+    // P of a buffer's round, p_full
+    uint64_t s_full[2][4], pv_done[2][4], p_full[3][2];
     // the V tiles to be cleaned: issued (so that the stage's barrier is in this
     // load's phase, not an older one of the same parity) and done; a slot per V
     // in the ring, as the cleaners run up to three tiles ahead of the products
@@ -85,7 +99,7 @@ struct Bars {
     uint32_t tmem;
     Item items[2];
 };
-static_assert(sizeof(Bars) <= 512, "barriers fit their room");
+static_assert(sizeof(Bars) <= 768, "barriers fit their room");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
                                             int32_t c2) {
@@ -129,13 +143,27 @@ __device__ __forceinline__ void mma_output(uint32_t d, uint32_t a, uint32_t b_lo
 template <int S>
 struct Ring {
     int st = 0, ph = 0;
-    __device__ __forceinline__ void next() {
-        if (++st == S) {
-            st = 0;
+    __device__ __forceinline__ void next(int n = 1) {
+        st += n;
+        if (st >= S) {
+            st -= S;
             ph ^= 1;
         }
     }
+    __device__ __forceinline__ void skip(int n) {
+        const int rounds = (st + n) / S;
+        st += n - rounds * S;
+        ph ^= rounds & 1;
+    }
 };
+
+// An item's loads come in the order K_0 K_1 V_0 K_2 V_1 ... K_{J-1} V_{J-2}
+// V_{J-1}: load i is K or V of key tile load_tile(i).
+__device__ __forceinline__ bool load_is_v(int i, int jmax) { return i == 2 * jmax - 1 || (i > 0 && (i & 1) == 0); }
+__device__ __forceinline__ int load_tile(int i, int jmax) {
+    return i == 2 * jmax - 1 ? jmax - 1 : (i & 1) ? (i + 1) >> 1 : i == 0 ? 0 : (i >> 1) - 1;
+}
+__device__ __forceinline__ int load_of_v(int j, int jmax) { return j < jmax - 1 ? 2 * j + 2 : 2 * jmax - 1; }
 
 template <typename T>
 constexpr uint32_t prompt_idesc(uint32_t n, bool b_mn_major) {
@@ -177,12 +205,8 @@ __device__ __forceinline__ Item find_item(const AttentionArgs& p, int index, int
             it.hk = local % p.Hk;
             it.token0 = (blocks - 1 - local / p.Hk) * 2 * tile_tokens;
             auto limit = [&](int token) { return p.causal ? clampi(token + s.m - s.n + 1, 0, s.m) : s.m; };
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int first = it.token0 + t * tile_tokens;
-                const int last = min(first + tile_tokens, s.n) - 1;
-                it.tiles[t] = first <= last ? (limit(last) + kKeyTile - 1) / kKeyTile : 0;
-            }
+            it.tiles = it.token0 + tile_tokens < s.n ? 2 : 1;
+            it.keys = (limit(min(it.token0 + 2 * tile_tokens, s.n) - 1) + kKeyTile - 1) / kKeyTile;
             it.edge = limit(it.token0) / kKeyTile;
             return it;
         }
@@ -215,12 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
                 mbar_init(&bars->q_full[t], 1);
                 mbar_init(&bars->q_empty[t], 1);
-                mbar_init(&bars->s_full[t], 1);
-                mbar_init(&bars->p_full[t][0], kSoftmaxWarps / 2);
-                mbar_init(&bars->p_full[t][1], kSoftmaxWarps / 2);
-                mbar_init(&bars->o_full[t], 1);
                 mbar_init(&bars->item_full[t], 1);
                 mbar_init(&bars->item_empty[t], kSoftmaxWarps + 3);  // and MMA, 2 cleaners
+            }
+            for (int i = 0; i < 8; ++i) {
+                mbar_init(&bars->s_full[i >> 2][i & 3], 1);
+                mbar_init(&bars->pv_done[i >> 2][i & 3], 1);
+            }
+            for (int i = 0; i < 3; ++i) {
+                mbar_init(&bars->p_full[i][0], kSoftmaxWarps / 2);
+                mbar_init(&bars->p_full[i][1], kSoftmaxWarps / 2);
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&bars->v_issued[i], 1);
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kSoftmaxWarps) {
         regs_dec<72>();
         if (warp == kSoftmaxWarps + 1) {
-            // ---- items and TMA loads: K_0 Q_0 Q_1 V_0 K_1 V_1 ...
+            // ---- items and TMA loads: K_0 Q_0 Q_1 K_1 V_0 ...
             if (elect_one_sync()) {
                 tma_prefetch_desc(&tmQ);
                 tma_prefetch_desc(&tmK);
@@ -271,25 +299,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!it.any) break;
                 if (lane == 0) index = atomicAdd(p.counters, 1);
-                const int jmax = max(it.tiles[0], it.tiles[1]);
+                const int jmax = it.keys;
                 for (int i = 0; i < 2 * jmax; ++i) {
-                    const int j = i >> 1;
+                    const int j = load_tile(i, jmax);
+                    const bool is_v = load_is_v(i, jmax);
                     ok = mbar_wait(&bars->kv_empty[r.st], r.ph, 61);
                     if (!ok) break;
                     if (elect_one_sync()) {
                         mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
-                        const void* map = (i & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+                        const void* map = is_v ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
 #pragma unroll
                         for (int c = 0; c < L::kChunks; ++c)
                             tma_load_3d(pipe + r.st * L::kTileBytes + c * kChunkBytes, map, &bars->kv_full[r.st],
                                         64 * c, it.hk, it.k0 + j * kKeyTile);
-                        if ((i & 1) && j >= it.edge) mbar_arrive(&bars->v_issued[(edges + j - it.edge) & 3]);
+                        if (is_v && j >= it.edge) mbar_arrive(&bars->v_issued[(edges + j - it.edge) & 3]);
                     }
                     r.next();
                     if (i == 0) {
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            if (it.tiles[t] == 0) continue;
+                            if (t >= it.tiles) continue;
                             ok = ok && mbar_wait(&bars->q_empty[t], q_ph[t], 62);
                             q_ph[t] ^= 1;
                             if (ok && elect_one_sync()) {
@@ -326,84 +355,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kSoftmaxWarps) {
             // ---- MMA issuer, one thread throughout (so that the MMAs' operands are uniform)
             if (elect_one_sync()) {
-            const uint32_t q_low = (smem_u32(smem) >> 4) | kDescKMajor, kv_low = pipe >> 4;
-            constexpr int kTileLow = L::kTileBytes >> 4;
-            auto scores = [&](int t, int st) {
-                const uint32_t a = q_low + t * kTileLow, b = (kv_low + st * kTileLow) | kDescKMajor;
+                constexpr int NB = L::kBuffers, kTileLow = L::kTileBytes >> 4;
+                const uint32_t q_low = (smem_u32(smem) >> 4) | kDescKMajor, kv_low = pipe >> 4;
+                int q_ph = 0, edges = 0, buf = 0, p_ph = 0, own[2] = {0, 0}, pv_own[2] = {0, 0};
+                Ring<S> r;  // the item's first load
+                bool ok = true;
+                // all steps of an item with kT tiles
+                auto run = [&](auto tc, int J, int edge) {
+                    constexpr int kT = decltype(tc)::value;
+                    Ring<S> rk = r, rv = r;  // the next K and V to use
+                    rv.next(load_of_v(0, J));
+                    auto scores = [&](int t, int j, int to) {
+                        const uint32_t a = q_low + t * kTileLow, b = (kv_low + rk.st * kTileLow) | kDescKMajor;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4;
-                    mma_scores(tmem + t * 128, a + off, b + off, prompt_idesc<T>(kKeyTile, false), k > 0);
-                }
-                mma_commit(&bars->s_full[t]);
-            };
-            int edges = 0, q_ph = 0, p_ph = 0;  // bit t: tile t's parity
-            Ring<S> r;
-            bool ok = true;
-            for (int at = 0; ok; ++at) {
-                if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 63)) break;
-                const volatile Item& it = bars->items[at & 1];
-                const int any = it.any, tiles0 = it.tiles[0], tiles1 = it.tiles[1], edge = it.edge;
-                if (!any) break;
-                mbar_arrive(&bars->item_empty[at & 1]);
-                const int jmax = max(tiles0, tiles1);
-                if (jmax == 0) continue;
-                ok = mbar_wait(&bars->kv_full[r.st], r.ph, 64);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    const int tiles = t ? tiles1 : tiles0;
-                    if (tiles == 0) continue;
-                    ok = mbar_wait(&bars->q_full[t], (q_ph >> t) & 1, 65);
-                    q_ph ^= 1 << t;
-                    tc_fence_after();
-                    if (ok) {
-                        scores(t, r.st);
-                        if (tiles == 1) mma_commit(&bars->q_empty[t]);
-                    }
-                }
-                if (ok) mma_commit(&bars->kv_empty[r.st]);
-                r.next();
-                for (int j = 0; j < jmax && ok; ++j) {
-                    const int vst = r.st;
-                    ok = mbar_wait(&bars->kv_full[r.st], r.ph, 66);
-                    r.next();
-                    if (ok && j >= edge) {
-                        ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67);
-                        ++edges;
-                    }
-                    const int kst = r.st;
-                    if (j + 1 < jmax) {
-                        ok = ok && mbar_wait(&bars->kv_full[r.st], r.ph, 68);
-                        r.next();
-                    }
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        const int tiles = t ? tiles1 : tiles0;
-                        if (j >= tiles) continue;
-                        const uint32_t b = (kv_low + vst * kTileLow) | kDescMnMajor;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            ok = ok && mbar_wait(&bars->p_full[t][half], (p_ph >> t) & 1, 69);
-                            tc_fence_after();
-                            if (!ok) break;
-#pragma unroll
-                            for (int k = 4 * half; k < 4 * half + 4; ++k)
-                                mma_output(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, b + k * (2048 >> 4),
-                                           prompt_idesc<T>(DP, true), j + k > 0);
+                        for (int k = 0; k < DP / 16; ++k) {
+                            const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4;
+                            mma_scores(tmem + 128 * to, a + off, b + off, prompt_idesc<T>(kKeyTile, false), k > 0);
                         }
-                        if (!ok) break;
-                        p_ph ^= 1 << t;
-                        if (j + 1 < tiles) {
-                            scores(t, kst);
-                            if (j + 2 == tiles) mma_commit(&bars->q_empty[t]);
-                        } else {
-                            mma_commit(&bars->o_full[t]);
+                        mma_commit(&bars->s_full[t][own[t] & 3]);
+                        ++own[t];
+                        if (j + 1 == J) mma_commit(&bars->q_empty[t]);
+                        if (t == kT - 1) {
+                            mma_commit(&bars->kv_empty[rk.st]);
+                            rk.next(j == 0 ? 1 : 2);
                         }
+                    };
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const int t = n % kT, j = n / kT;
+                        if (j >= J) break;
+                        if (t == 0 && !(ok = mbar_wait(&bars->kv_full[rk.st], rk.ph, 64))) return;
+                        if (j == 0 && !(ok = mbar_wait(&bars->q_full[t], (q_ph >> t) & 1, 65))) return;
+                        tc_fence_after();
+                        const int to = buf + n;
+                        scores(t, j, to >= NB ? to - NB : to);
                     }
-                    if (ok) {
-                        mma_commit(&bars->kv_empty[vst]);
-                        if (j + 1 < jmax) mma_commit(&bars->kv_empty[kst]);
+                    q_ph ^= (1 << kT) - 1;
+                    for (int j = 0; j < J; ++j) {
+                        if (!(ok = mbar_wait(&bars->kv_full[rv.st], rv.ph, 66))) return;
+                        if (j >= edge) {
+                            if (!(ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67))) return;
+                            ++edges;
+                        }
+                        const uint32_t v_low = (kv_low + rv.st * kTileLow) | kDescMnMajor;
+#pragma unroll
+                        for (int t = 0; t < kT; ++t) {
+                            // S of step n + NB: (nt, nj)
+                            const int nt = (t + NB) % kT, nj = j + (t + NB) / kT;
+                            if (nt == 0 && nj < J && !(ok = mbar_wait(&bars->kv_full[rk.st], rk.ph, 68))) return;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (!(ok = mbar_wait(&bars->p_full[buf][half], (p_ph >> buf) & 1, 69))) return;
+                                tc_fence_after();
+#pragma unroll
+                                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                    mma_output(tmem + L::kOutputs + t * DP, tmem + 128 * buf + 8 * k,
+                                               v_low + k * (2048 >> 4), prompt_idesc<T>(DP, true), j + k > 0);
+                            }
+                            if (nj < J) scores(nt, nj, buf);
+                            mma_commit(&bars->pv_done[t][pv_own[t] & 3]);
+                            ++pv_own[t];
+                            p_ph ^= 1 << buf;
+                            if (++buf == NB) buf = 0;
+                        }
+                        mma_commit(&bars->kv_empty[rv.st]);
+                        rv.next(load_of_v(j + 1, J) - load_of_v(j, J));
                     }
+                };
+                for (int at = 0; ok; ++at) {
+                    if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 63)) break;
+                    const volatile Item& it = bars->items[at & 1];
+                    const int any = it.any, two = it.tiles > 1, J = it.keys, edge = it.edge;
+                    if (!any) break;
+                    mbar_arrive(&bars->item_empty[at & 1]);
+                    if (J == 0) continue;
+                    if (two) run(std::integral_constant<int, 2>{}, J, edge);
+                    else run(std::integral_constant<int, 1>{}, J, edge);
+                    r.skip(2 * J);
                 }
-            }
             // every commit has arrived before the CTA ends
             mma_commit(&bars->done);
             mbar_wait(&bars->done, 0, 70);
@@ -418,14 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 71)) break;
                 volatile Item& it = bars->items[at & 1];
                 if (!it.any) break;
-                const int jmax = max(it.tiles[0], it.tiles[1]);
+                const int jmax = it.keys;
                 for (int j = it.edge; j < jmax && ok; ++j, ++edges) {
-                    const int lv = ld + 2 * j + 1;
+                    const int lv = ld + load_of_v(j, jmax);
                     ok = mbar_wait(&bars->v_issued[edges & 3], (edges >> 2) & 1, 72) &&
                          mbar_wait(&bars->kv_full[lv % S], (lv / S) & 1, 73);
                     if (!ok) break;
                     const uint32_t v = pipe + (lv % S) * L::kTileBytes;
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = me; c < L::kTileBytes / 16; c += 64) {
                         uint4 w;
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -462,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_token = t * tile_tokens + row / p.group, row_head = row % p.group;
         const bool used = row < tile_tokens * p.group;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        const uint32_t to = tmem + lanes + L::kOutputs + t * DP;
         const float c = p.scale_log2;
         const uint64_t c2 = f2_pack(c, c);
-        int s_ph = 0, o_ph = 0;
+        int steps = 0, own = 0;  // steps of both tiles before this item (mod the buffers), of this tile
         bool ok = true;
         for (int at = 0; ok; ++at) {
             if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 74)) break;
@@ -478,13 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lim = valid ? (p.causal ? clampi(token + m - n + 1, 0, m) : m) : 0;
                 warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : m);
             }
-            const int tiles = it.tiles[t];
+            const int both = it.tiles, tiles = t < both ? it.keys : 0;
             float ref = -INFINITY;
             uint64_t sum2 = f2_pack(0.0f, 0.0f);
-            for (int j = 0; j < tiles; ++j) {
-                ok = mbar_wait(&bars->s_full[t], s_ph, 75);
+            for (int j = 0; j < tiles; ++j, ++own) {
+                const int buf = (steps + j * both + t) % L::kBuffers;
+                const uint32_t ts = tmem + lanes + 128 * buf;
+                ok = mbar_wait(&bars->s_full[t][own & 3], (own >> 2) & 1, 75);
                 if (!ok) break;
-                s_ph ^= 1;
                 tc_fence_after();
                 uint32_t v[4][32];
 #pragma unroll
@@ -492,12 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_wait_ld_regs32(v[i]);
                 if (warp_lim < (j + 1) * kKeyTile) {
-                    const int left = lim - j * kKeyTile;  // columns this row sees
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        const int left = lim - j * kKeyTile - 32 * i;  // columns this row sees
+                        if (!__any_sync(0xffffffffu, left < 32)) continue;
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (32 * i + k >= left) v[i][k] = 0xFF800000u;  // -inf
+                            if (k >= left) v[i][k] = 0xFF800000u;  // -inf
+                    }
                 }
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -514,6 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float f = moves ? exp2_approx(ref - top) : 1.0f;
                         if (moves) ref = top;
                         sum2 = f2_mul(sum2, f2_pack(f, f));
+                        // S of this step says nothing of the product before it
+                        ok = mbar_wait(&bars->pv_done[t][(own - 1) & 3], ((own - 1) >> 2) & 1, 77);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int i = 0; i < DP / 16; ++i) {
                             uint32_t o[16];
@@ -546,20 +582,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->p_full[t][i >> 1]);
+                        if (lane == 0) mbar_arrive(&bars->p_full[buf][i >> 1]);
                     }
                 }
                 sum2 = f2_add(part2[0], part2[1]);
             }
 
+            steps = (steps + both * it.keys) % L::kBuffers;
+
             // ---- O / sum to memory
             float l0, l1;
             f2_unpack(sum2, l0, l1);
             const float l = l0 + l1;
-            if (tiles > 0) {
-                ok = ok && mbar_wait(&bars->o_full[t], o_ph, 76);
-                o_ph ^= 1;
-            }
+            if (tiles > 0) ok = ok && mbar_wait(&bars->pv_done[t][(own - 1) & 3], ((own - 1) >> 2) & 1, 76);
             if (!ok) break;
             tc_fence_after();
             const int bad = tiles > 0 ? it.bad : 0;
@@ -568,39 +603,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             leave_item(at);
             const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
             const int head = hk * p.group + row_head;
-            T* dst = static_cast<T*>(p.o) + static_cast<int64_t>(q0 + token) * p.o_token +
-                     static_cast<int64_t>(head) * p.o_head;
+            const int64_t mine = static_cast<int64_t>(q0 + token) * p.o_token + static_cast<int64_t>(head) * p.o_head;
+            // through shared memory, so that eight lanes write 128 bytes of a row
+            const uint32_t stage = smem_u32(smem) + L::kOut + warp * L::kOutBytes;
+            const int sub = lane >> 3, ch = lane & 7;
 #pragma unroll 1
-            for (int i = 0; i < DP / 32; ++i) {
-                uint32_t o[32];
-                const int col = 32 * i;
-                if (tiles > 0) {
-                    tmem_ld_32x32b_x32(to + 32 * i, o);
-                    tmem_wait_ld_regs32(o);
-                }
-                if (bad) {
-                    for (int key = edge * kKeyTile; key < lim; ++key) {
-                        const T* src = static_cast<const T*>(p.v) + static_cast<int64_t>(k0 + key) * p.v_token +
-                                       static_cast<int64_t>(hk) * p.v_head + col;
+            for (int i = 0; i < DP / 64; ++i) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            if (col + x >= p.D) continue;
-                            const float val = static_cast<float>(src[x]);
-                            if (!isfinite(val)) o[x] = __float_as_uint(__uint_as_float(o[x]) + val);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[32];
+                    if (tiles > 0) {
+                        tmem_ld_32x32b_x32(to + 64 * i + 32 * q, o);
+                        tmem_wait_ld_regs32(o);
+                    }
+                    if (bad) {
+                        for (int key = edge * kKeyTile; key < lim; ++key) {
+                            const T* src = static_cast<const T*>(p.v) + static_cast<int64_t>(k0 + key) * p.v_token +
+                                           static_cast<int64_t>(hk) * p.v_head + 64 * i + 32 * q;
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) {
+                                if (64 * i + 32 * q + x >= p.D) continue;
+                                const float val = static_cast<float>(src[x]);
+                                if (!isfinite(val)) o[x] = __float_as_uint(__uint_as_float(o[x]) + val);
+                            }
                         }
                     }
-                }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t w[4];
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        w[x] = lim > 0 ? Pair16<T>::pack(__uint_as_float(o[8 * h + 2 * x]) * inv,
-                                                         __uint_as_float(o[8 * h + 2 * x + 1]) * inv)
-                                       : 0u;
-                    if (valid && col + 8 * h < p.D)
-                        *reinterpret_cast<uint4*>(dst + col + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = lim > 0 ? Pair16<T>::pack(__uint_as_float(o[8 * h + 2 * x]) * inv,
+                                                             __uint_as_float(o[8 * h + 2 * x + 1]) * inv)
+                                           : 0u;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         stage + lane * 128 + (((4 * q + h) ^ (lane & 7)) << 4)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += 4) {
+                    const int r = r0 + sub;
+                    const int64_t at_r = __shfl_sync(0xffffffffu, mine, r);
+                    const bool take = __shfl_sync(0xffffffffu, valid, r) && 64 * i + 8 * ch < p.D;
+                    uint4 w;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                 : "r"(stage + r * 128 + ((ch ^ (r & 7)) << 4))
+                                 : "memory");
+                    if (take) *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + at_r + 64 * i + 8 * ch) = w;
+                }
+                __syncwarp();
             }
             if (p.lse && valid)
                 p.lse[static_cast<int64_t>(q0 + token) * p.Hq + head] =
