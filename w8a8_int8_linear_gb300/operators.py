@@ -11,6 +11,7 @@ synchronizes, so every call can be captured into a CUDA graph.
 import math
 
 import torch
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
 
 from . import RMS_NORM, _check, lib
 
@@ -21,32 +22,33 @@ _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUT = {HALF: 0, INTERLEAVED: 1}
 
 
-def _heads(t, name, like=None):
-    """Checks a [tokens, heads, dim] tensor: on the GPU, 16-bit, dense last
-    dimension.  Returns its token and head strides; a dimension of one row has
-    no stride of its own and gets the row length."""
+def _heads(t, name, dtype=None):
+    """Checks a [tokens, heads, dim] tensor: on the GPU, 16-bit (of `dtype`),
+    dense last dimension.  Returns its token and head strides; a dimension of
+    one row has no stride of its own and gets the row length."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if like is None:
+    if t.dtype is not dtype:
+        if dtype is not None:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
             raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    elif t.dtype is not like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) != 3:
+    strides = t.stride()
+    if len(strides) != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
-    st, sh, sd = t.stride()
-    if sd != 1 and shape[2] != 1:
+    token, head, last = strides
+    tokens, heads, dim = t.shape
+    if last != 1 and dim != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
-    return (st if shape[0] != 1 else shape[1] * shape[2]), (sh if shape[1] != 1 else shape[2])
+    return (token if tokens != 1 else heads * dim), (head if heads != 1 else dim)
 
 
 def _indices(t, dtype, n, name):
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if not t.is_cuda or not t.is_contiguous() or t.dim() != 1 or t.numel() != n:
+    if not t.is_cuda or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a dense CUDA tensor of {n} values")
     return t.data_ptr()
 
@@ -64,10 +66,9 @@ def attention_workspace(device=None):
 def _workspace_of(device, stream):
     if torch.cuda.is_current_stream_capturing():
         return attention_workspace(device)  # the graph's own, zeroed by every replay
-    key = (device, stream)
-    ws = _attention_ws.get(key)
+    ws = _attention_ws.get((device.index, stream))
     if ws is None:
-        ws = _attention_ws[key] = attention_workspace(device)
+        ws = _attention_ws[device.index, stream] = attention_workspace(device)
     return ws
 
 
@@ -89,8 +90,9 @@ def attention(Q, K, V, cu_q=None, cu_k=None, k_lens=None, batch=1, causal=True, 
     workspace (`attention_workspace()`) is by default one per stream, and one
     of its own for a captured call."""
     q_token, q_head = _heads(Q, "Q")
-    k_token, k_head = _heads(K, "K", Q)
-    v_token, v_head = _heads(V, "V", Q)
+    dtype, device = Q.dtype, Q.device
+    k_token, k_head = _heads(K, "K", dtype)
+    v_token, v_head = _heads(V, "V", dtype)
     tq, hq, d = Q.shape
     tk, hk, dk = K.shape
     if dk != d or V.shape != K.shape:
@@ -103,18 +105,18 @@ def attention(Q, K, V, cu_q=None, cu_k=None, k_lens=None, batch=1, causal=True, 
     pk = None if cu_k is None else _indices(cu_k, torch.int32, batch + 1, "cu_k")
     pl = None if k_lens is None else _indices(k_lens, torch.int32, batch, "k_lens")
     if out is None:
-        out = torch.empty((tq, hq, d), dtype=Q.dtype, device=Q.device)
+        out = torch.empty((tq, hq, d), dtype=dtype, device=device)
         o_token, o_head = hq * d, d
     else:
-        o_token, o_head = _heads(out, "out", Q)
+        o_token, o_head = _heads(out, "out", dtype)
         if out.shape != Q.shape:
             raise ValueError("out must have the shape of Q")
-    stats = torch.empty((tq, hq), dtype=torch.float32, device=Q.device) if lse else None
-    stream = torch.cuda.current_stream().cuda_stream
-    ws = _workspace_of(Q.device, stream) if workspace is None else workspace
+    stats = torch.empty((tq, hq), dtype=torch.float32, device=device) if lse else None
+    stream = _raw_stream(device.index)
+    ws = _workspace_of(device, stream) if workspace is None else workspace
     _check("w8a8_attention", lib().w8a8_attention(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), out.data_ptr(), None if stats is None else stats.data_ptr(), pq, pk,
-        pl, _DTYPE[Q.dtype], batch, tq, tk, hq, hk, d, q_token, q_head, k_token, k_head, v_token, v_head, o_token,
+        pl, _DTYPE[dtype], batch, tq, tk, hq, hk, d, q_token, q_head, k_token, k_head, v_token, v_head, o_token,
         o_head, d ** -0.5 if scale is None else scale, causal, ws.data_ptr(), ws.numel(), stream))
     return (out, stats) if lse else out
 
@@ -176,21 +178,30 @@ def rotary(Q, K, positions, freqs, layout=HALF, amplitude=1.0, inverse=False, q_
     themselves.  inverse=True turns back (also the gradient's direction, at
     amplitude 1)."""
     q_token, q_head = _heads(Q, "Q")
-    k_token, k_head = (0, 0) if K is None else _heads(K, "K", Q)
+    dtype, device = Q.dtype, Q.device
     t, hq, d, pp, pf, rot = _rotary_common(Q, K, positions, freqs, layout)
-    hk = 0 if K is None else K.shape[1]
+    hk = k_token = k_head = ko_token = ko_head = 0
+    if K is not None:
+        hk = K.shape[1]
+        k_token, k_head = _heads(K, "K", dtype)
+        if k_out is None:
+            k_out = torch.empty((t, hk, d), dtype=dtype, device=device)
+            ko_token, ko_head = hk * d, d
+        else:
+            ko_token, ko_head = _heads(k_out, "k_out", dtype)
+            if k_out.shape != K.shape:
+                raise ValueError("k_out must have the shape of K")
     if q_out is None:
-        q_out = torch.empty((t, hq, d), dtype=Q.dtype, device=Q.device)
-    if k_out is None and K is not None:
-        k_out = torch.empty((t, hk, d), dtype=Q.dtype, device=Q.device)
-    qo_token, qo_head = _heads(q_out, "q_out", Q)
-    ko_token, ko_head = (0, 0) if K is None else _heads(k_out, "k_out", Q)
-    if q_out.shape != Q.shape or (K is not None and k_out.shape != K.shape):
-        raise ValueError("the outputs must have the shapes of Q and K")
+        q_out = torch.empty((t, hq, d), dtype=dtype, device=device)
+        qo_token, qo_head = hq * d, d
+    else:
+        qo_token, qo_head = _heads(q_out, "q_out", dtype)
+        if q_out.shape != Q.shape:
+            raise ValueError("q_out must have the shape of Q")
     _check("w8a8_rotary", lib().w8a8_rotary(
         Q.data_ptr(), None if K is None else K.data_ptr(), q_out.data_ptr(), None if K is None else k_out.data_ptr(),
-        _DTYPE[Q.dtype], t, hq, hk, d, rot, q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head,
-        pp, pf, amplitude, _LAYOUT[layout], inverse, torch.cuda.current_stream().cuda_stream))
+        _DTYPE[dtype], t, hq, hk, d, rot, q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head,
+        pp, pf, amplitude, _LAYOUT[layout], inverse, _raw_stream(device.index)))
     return q_out, (None if K is None else k_out)
 
 
@@ -200,27 +211,28 @@ def rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, layout=HAL
     a slot outside the cache (-1 for a padding token) stores nothing.  Returns
     the turned Q."""
     q_token, q_head = _heads(Q, "Q")
-    k_token, k_head = _heads(K, "K", Q)
-    v_token, v_head = _heads(V, "V", Q)
-    kc_token, kc_head = _heads(k_cache, "k_cache", Q)
-    vc_token, vc_head = _heads(v_cache, "v_cache", Q)
+    dtype, device = Q.dtype, Q.device
+    k_token, k_head = _heads(K, "K", dtype)
+    v_token, v_head = _heads(V, "V", dtype)
+    kc_token, kc_head = _heads(k_cache, "k_cache", dtype)
+    vc_token, vc_head = _heads(v_cache, "v_cache", dtype)
     t, hq, d, pp, pf, rot = _rotary_common(Q, K, positions, freqs, layout)
     hk = K.shape[1]
     if V.shape != K.shape or k_cache.shape[1:] != K.shape[1:] or v_cache.shape != k_cache.shape:
         raise ValueError("V must have the shape of K, and both caches its heads and dim")
     ps = _indices(slots, torch.int64, t, "slots")
     if q_out is None:
-        q_out = torch.empty((t, hq, d), dtype=Q.dtype, device=Q.device)
+        q_out = torch.empty((t, hq, d), dtype=dtype, device=device)
         qo_token, qo_head = hq * d, d
     else:
-        qo_token, qo_head = _heads(q_out, "q_out", Q)
+        qo_token, qo_head = _heads(q_out, "q_out", dtype)
         if q_out.shape != Q.shape:
             raise ValueError("q_out must have the shape of Q")
     _check("w8a8_rotary_append", lib().w8a8_rotary_append(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        _DTYPE[Q.dtype], t, hq, hk, d, rot, k_cache.shape[0], q_token, q_head, k_token, k_head, v_token, v_head,
+        _DTYPE[dtype], t, hq, hk, d, rot, k_cache.shape[0], q_token, q_head, k_token, k_head, v_token, v_head,
         qo_token, qo_head, kc_token, kc_head, vc_token, vc_head, pp, ps, pf, amplitude, _LAYOUT[layout],
-        torch.cuda.current_stream().cuda_stream))
+        _raw_stream(device.index)))
     return q_out
 
 
@@ -232,6 +244,32 @@ def _rows(t, name, dtype, shape):
     if not t.is_cuda or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a dense CUDA tensor of shape {tuple(shape)}")
     return t.data_ptr()
+
+
+def _modulation(tensors, k, m, rows_per_group):
+    """Pointers of gate, mod_scale and mod_shift ([groups, k] or [k]) and the
+    row stride that they share."""
+    pointers, strides = [], set()
+    for t, name in zip(tensors, ("gate", "mod_scale", "mod_shift")):
+        if t is None:
+            pointers.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a torch.bfloat16 CUDA tensor")
+        if t.dim() == 1:
+            t = t.unsqueeze(0)
+        if t.dim() != 2 or t.shape[1] != k or (k != 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [groups, {k}], dense in its last dimension")
+        groups = t.shape[0]
+        if groups * rows_per_group < m and not (groups == 1 and rows_per_group == 0):
+            raise ValueError(f"{name} has {groups} rows of {rows_per_group} tokens each, too few for {m} tokens")
+        # a single row serves every token, and its stride is not used
+        if rows_per_group and m > rows_per_group:
+            strides.add(t.stride(0))
+        pointers.append(t.data_ptr())
+    if len(strides) > 1:
+        raise ValueError("gate, mod_scale and mod_shift must have the same row stride")
+    return pointers, strides.pop() if strides else 0
 
 
 def residual_norm_quant(X, B, gamma=None, beta=None, eps=1e-6, kind=RMS_NORM, alpha=1.0, gate=None, branch_gamma=None,
@@ -255,31 +293,16 @@ def residual_norm_quant(X, B, gamma=None, beta=None, eps=1e-6, kind=RMS_NORM, al
     if X.dtype is not torch.bfloat16 and X.dtype is not torch.float32:
         raise TypeError(f"X must be torch.bfloat16 or torch.float32, got {X.dtype}")
     m, k = X.shape
-    px = _rows(X, "X", X.dtype, X.shape)
-    pb = _rows(B, "B", torch.bfloat16, X.shape)
-    vec = [None if t is None else _rows(t, name, torch.bfloat16, (k,))
-           for t, name in ((branch_gamma, "branch_gamma"), (gamma, "gamma"), (beta, "beta"))]
-    mod, stride = [], None
-    for t, name in ((gate, "gate"), (mod_scale, "mod_scale"), (mod_shift, "mod_shift")):
-        if t is None:
-            mod.append(None)
-            continue
-        if t.dtype is not torch.bfloat16 or not t.is_cuda:
-            raise TypeError(f"{name} must be a torch.bfloat16 CUDA tensor")
-        if t.dim() == 1:
-            t = t.unsqueeze(0)
-        groups = t.shape[0]
-        if t.dim() != 2 or t.shape[1] != k or (k != 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be [groups, {k}], dense in its last dimension")
-        if groups > 1:
-            if stride is not None and stride != t.stride(0):
-                raise ValueError("gate, mod_scale and mod_shift must have the same row stride")
-            stride = t.stride(0)
-        if groups * rows_per_group < m and not (groups == 1 and rows_per_group == 0):
-            raise ValueError(f"{name} has {groups} rows of {rows_per_group} tokens each, too few for {m} tokens")
-        mod.append((t.data_ptr(), groups))
-    if stride is not None and any(x is not None and x[1] == 1 for x in mod) and m > rows_per_group:
-        raise ValueError("gate, mod_scale and mod_shift must have the same number of rows")
+    shape, row = X.shape, (k,)
+    px = _rows(X, "X", X.dtype, shape)
+    pb = _rows(B, "B", torch.bfloat16, shape)
+    pbg = None if branch_gamma is None else _rows(branch_gamma, "branch_gamma", torch.bfloat16, row)
+    pga = None if gamma is None else _rows(gamma, "gamma", torch.bfloat16, row)
+    pbe = None if beta is None else _rows(beta, "beta", torch.bfloat16, row)
+    pg = ps = pt = None
+    stride = 0
+    if gate is not None or mod_scale is not None or mod_shift is not None:
+        (pg, ps, pt), stride = _modulation((gate, mod_scale, mod_shift), k, m, rows_per_group)
     if h_out is None:
         h_out = torch.empty_like(X)
         ph = h_out.data_ptr()
@@ -290,10 +313,9 @@ def residual_norm_quant(X, B, gamma=None, beta=None, eps=1e-6, kind=RMS_NORM, al
     Xq = torch.empty((m, k), dtype=torch.int8, device=dev) if codes else None
     Y = torch.empty((m, k), dtype=torch.bfloat16, device=dev) if y else None
     sx = torch.empty((m,), dtype=torch.float32, device=dev) if image or codes else None
-    pg, ps, pt = (None if x is None else x[0] for x in mod)
     _check("w8a8_residual_norm_quant", lib().w8a8_residual_norm_quant(
-        px, pb, ph, _DTYPE[X.dtype], *vec, pg, ps, pt, stride or 0, rows_per_group, alpha, eps, kind, m, k,
+        px, pb, ph, _DTYPE[X.dtype], pbg, pga, pbe, pg, ps, pt, stride, rows_per_group, alpha, eps, kind, m, k,
         None if Y is None else Y.data_ptr(), None if Xq is None else Xq.data_ptr(),
         None if Ximg is None else Ximg.data_ptr(), None if sx is None else sx.data_ptr(),
-        torch.cuda.current_stream().cuda_stream))
+        _raw_stream(dev.index)))
     return h_out, Ximg, sx, Xq, Y
