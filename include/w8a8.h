@@ -351,8 +351,8 @@ typedef enum { W8A8_BF16 = 0, W8A8_FP16 = 1, W8A8_FP32 = 2 } w8a8_dtype;
  * Products are summed, and the softmax and its output held, in binary32; the
  * weights exp(t) enter the second product rounded to the inputs' type.
  *   Q [Tq,Hq,D], K, V [Tk,Hk,D], O [Tq,Hq,D]: dtype BF16 or FP16, the last
- *   dimension dense, token and head strides in elements (multiples of 8);
- *   D % 8 == 0 and D <= 128, Hq % Hk == 0.  O must not overlap the inputs.
+ *   dimension dense, token and head strides in elements (positive multiples of 8
+ *   below 2^39); D % 8 == 0 and D <= 128, Hq % Hk == 0.  O must not overlap the inputs.
  *   lse [Tq,Hq] fp32 out or NULL.
  *   cu_q, cu_k [batch+1] int32 (device) or NULL: rows cu[b] .. cu[b+1] are
  *   sequence b's; NULL: batch equal parts of Tq / Tk rows (else

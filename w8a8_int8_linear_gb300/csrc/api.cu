@@ -619,14 +619,15 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
     if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
     if (batch < 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return W8A8_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
-    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || Tk > INT32_MAX || batch > INT32_MAX)
+    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || Tk > INT32_MAX ||
+        batch > INT32_MAX || Tq * (Hq / Hk) > INT32_MAX)
         return W8A8_ERR_SHAPE;
     if (batch == 0 || Tq == 0) return W8A8_OK;
     if ((!cu_q && Tq % batch != 0) || (!cu_k && Tk % batch != 0)) return W8A8_ERR_SHAPE;
     if (!Q || !O || (Tk > 0 && (!K || !V))) return W8A8_ERR_INVALID_ARG;
     const int64_t strides[8] = {q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head};
     for (int64_t v : strides)
-        if (v < 0 || v % 8 != 0) return W8A8_ERR_ALIGNMENT;
+        if (v <= 0 || v >= (int64_t(1) << 39) || v % 8 != 0) return W8A8_ERR_ALIGNMENT;
     if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lse) || !aligned4(cu_q) ||
         !aligned4(cu_k) || !aligned4(k_lens))
         return W8A8_ERR_ALIGNMENT;
@@ -663,17 +664,15 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.causal = causal != 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (Tq * a.group >= 32 * batch && w8a8::attention_prompt_takes(a)) {
-        void* enc = encode_fn();
-        if (!enc) return W8A8_ERR_CUDA;
-        t_detail[0] = 0;
-        const cudaError_t e = w8a8::launch_attention_prompt(a, dtype, dev.num_sms, workspace, enc, st, t_detail,
-                                                            sizeof t_detail);
-        if (e == cudaSuccess) return W8A8_OK;
-        cudaGetLastError();
-        return t_detail[0] ? W8A8_ERR_CUDA : cuda_fail("attention launch", e);
-    }
-    return from_cuda(w8a8::launch_attention(a, dtype, dev.num_sms, workspace, st), "attention launch");
+    void* enc = encode_fn();
+    if (!enc) return W8A8_ERR_CUDA;
+    t_detail[0] = 0;
+    const auto launch =
+        w8a8::attention_splits(a, dev.num_sms) ? w8a8::launch_attention_split : w8a8::launch_attention_prompt;
+    const cudaError_t e = launch(a, dtype, dev.num_sms, workspace, enc, st, t_detail, sizeof t_detail);
+    if (e == cudaSuccess) return W8A8_OK;
+    cudaGetLastError();
+    return t_detail[0] ? W8A8_ERR_CUDA : cuda_fail("attention launch", e);
 }
 
 }  // extern "C"
@@ -831,6 +830,7 @@ w8a8_status w8a8_get_device_error(int* code) {
     if (w8a8::quant_read_device_error(&vq) != cudaSuccess) return W8A8_ERR_CUDA;
     unsigned int va = 0, vr = 0;
     if (w8a8::attention_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
+    if (va == 0 && w8a8::attention_split_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
     if (w8a8::residual_norm_read_device_error(&vr) != cudaSuccess) return W8A8_ERR_CUDA;
     if (v == 0) v = vs;
     if (v == 0) v = vq;

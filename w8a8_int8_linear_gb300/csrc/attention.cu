@@ -3,25 +3,28 @@
 //
 // One query of a group of G heads reads each K and V value once for G
 // multiply-adds, so the keys' bytes bound it: the G heads (and the n queries)
-// that share a KV head form the rows of one or two warp MMA tiles (16 x 16 x 8)
+// that share a KV head form the rows of up to four warp MMA tiles (16 x 16 x 8)
 // and the keys stream through shared memory once.
 //
 // The row blocks of all sequences are laid end to end, each as its tiles of 64
 // keys, and cut into equal ranges whatever the lengths are; the lengths stay on
-// the device.  CTA c takes range c / Hk for KV head c mod Hk, so that the CTAs
-// that run side by side read the neighbouring heads of the same keys (whole
-// rows of the cache).  Within a CTA each warp runs its own online softmax over
-// its own 16 keys of every tile (no barrier while keys stream), and the four
-// are joined at the end of an item.  An item that spans CTAs leaves (max, sum,
-// unnormalized output) per piece in the workspace; the CTA that arrives last
-// joins the pieces in key order, so the result does not depend on the order of
-// arrival.
+// the device.  CTAs that run side by side take the same range for neighbouring
+// KV heads (up to 8), so that they read whole rows of the cache.  One CTA per
+// SM: warp 8 keeps the ring of key tiles full by TMA, also across items; warps
+// 0-3 and 4-7 take the tiles in turn, each warp its own 16 rows and its own part
+// of the tile's keys with an online softmax of its own (no barrier while keys
+// stream), and are joined at the end of an item.  An item that spans CTAs leaves (max, sum, unnormalized output)
+// per piece in the workspace; the CTA that arrives last joins the pieces in key
+// order, so the result does not depend on the order of arrival.
 //
 //   softmax:  t = scale log2(e) s;  running max M, sum L, O in binary32,
 //             p = 2^(t - M); P enters the second product rounded to the
 //             inputs' type (half a step, 2^-8 for bf16, of each p: the same
 //             size as the output's own rounding, the sums stay binary32).
-#include <cfloat>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstdio>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -32,26 +35,36 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kKeys = 16;      // keys of a warp per tile
-constexpr int kTile = kWarps * kKeys;
-constexpr int kStages = 3;
+constexpr int kGroups = 2;     // of consumer warps, which take tiles in turn
+constexpr int kWarps = 4;      // of a group
+constexpr int kKeys = 16;      // keys of a step
+constexpr int kTile = 64;
+constexpr int kConsumers = kGroups * kWarps * 32;
 
-// R: packed (query, head) rows of an item, 16 or 32.
+// R: packed (query, head) rows of an item: 16, 32 or 64.  The four warps of a
+// group are R / 16 tiles of rows by 64 / R parts of the keys.
 template <int DP, int R>
 struct SplitSmem {
-    static constexpr int kStageBytes = 2 * kKeys * DP * 2;  // K and V of one warp
-    static constexpr int kPipe = kWarps * kStages * kStageBytes;
-    static constexpr int kQ = R * DP * 2;
-    static constexpr int kJoin = kWarps * R * (DP + 2) * 4;  // reuses the pipe
-    static constexpr int kTotal = (kPipe > kJoin ? kPipe : kJoin) + kQ;
+    static constexpr int kChunk = kTile * 128;  // 64 elements of each key, 128-byte swizzled
+    static constexpr int kKv = DP / 64 * kChunk;
+    static constexpr int kStage = 2 * kKv;      // K, then V
+    // even: a stage is always the same group's, whose waits then see every round of its barrier
+    static constexpr int kStages = DP == 128 ? 4 : 8;
+    static_assert(kStages % kGroups == 0, "one group per stage");
+    static constexpr int kJoin = kStages * kStage;  // (max, sum, output) of four warps
+    static constexpr int kQ = kJoin + kWarps * 16 * (DP + 2) * 4;
+    static constexpr int kBars = kQ + R * DP * 2;
+    static constexpr int kTotal = kBars + 2 * kStages * 8;
 };
 
-// Byte offset of 16-byte chunk c of row r in a [rows][DP] tile: chunks
-// permuted by the row, so that eight rows of one chunk column fall into
-// different banks.
+// Byte offset of 16-byte chunk c of row r of a tile as TMA writes it, and of a
+// [rows][DP] tile of Q: chunks permuted by the row, so that eight rows of one
+// chunk column fall into different banks.
+__device__ __forceinline__ uint32_t kv_at(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
 template <int DP>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
+__device__ __forceinline__ uint32_t q_at(int r, int c) {
     return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
 }
 
@@ -59,13 +72,13 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 template <int DP, int R>
 constexpr int kPartFloats = R * (DP + 2);
 
-// Where a linear tile index lies: sequence, row block, tile of the block.
+// Where a linear tile index lies: sequence, head group and row block, tile.
 struct Cursor {
     int b;
     Sequence s;
     int blocks;    // R-row blocks of the sequence
     int tiles;     // key tiles of one block
-    int block;
+    int item;      // head group * blocks + block
     int tile;
 };
 
@@ -82,7 +95,7 @@ __device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64
     mine = 0;
     if (b0 + lane < p.batch) {
         const Sequence s = sequence(p, b0 + lane);
-        mine = static_cast<int64_t>(blocks_of<R>(p, s)) * tiles_of(s);
+        mine = static_cast<int64_t>(blocks_of<R>(p, s)) * (p.Hk / p.side_heads) * tiles_of(s);
     }
     incl = mine;
 #pragma unroll
@@ -92,22 +105,44 @@ __device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64
     }
 }
 
+// a / b for positive a and b, in 32 bits where a allows.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 template <typename T, int DP, int R>
-__global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const AttentionArgs p) {
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kConsumers + 32, 1)
+    attention_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                           const AttentionArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int last_flag;
     using L = SplitSmem<DP, R>;
-    constexpr int kMT = R / 16;       // MMA tiles of rows
+    constexpr int S = L::kStages;
+    constexpr int kRowTiles = R / 16, kParts = kWarps / kRowTiles;
     constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
     constexpr int kDT = DP / 8;       // 8-wide output column tiles
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int dchunks = p.D >> 3;
-    uint8_t* q_smem = smem + L::kTotal - L::kQ;
-    uint8_t* pipe = smem + warp * kStages * L::kStageBytes;
-    float* join = reinterpret_cast<float*>(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* empty = full + S;
+    float* join = reinterpret_cast<float*>(smem + L::kJoin);
 
-    const int hk = blockIdx.x % p.Hk, range = blockIdx.x / p.Hk, ranges = gridDim.x / p.Hk;
-    // all tiles, by every warp on its own; the first 32 sequences' counts stay
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles start at multiples of 1024
+        if (threadIdx.x == 0) record_device_error(1);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWarps);
+        }
+        fence_mbarrier_init();
+    }
+
+    // this CTA's range of tiles, found by every warp on its own; the first 32
+    // sequences' counts stay
+    const int side = blockIdx.x % p.side_heads, range = blockIdx.x / p.side_heads, ranges = gridDim.x / p.side_heads;
+    const int head_groups = p.Hk / p.side_heads;
     int64_t mine, incl;
     tiles_from<R>(p, 0, mine, incl);
     int64_t total = __shfl_sync(0xffffffffu, incl, 31);
@@ -116,7 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const A
         tiles_from<R>(p, b0, m2, i2);
         total += __shfl_sync(0xffffffffu, i2, 31);
     }
-    const int64_t per = max(static_cast<int64_t>(p.min_tiles), (total + ranges - 1) / ranges);
+    const int64_t per = max(int64_t(1), quotient(total + ranges - 1, ranges));
     int64_t w = per * range;
     const int64_t w_end = min(total, w + per);
     if (w >= w_end) return;
@@ -137,247 +172,285 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const A
         c.s = sequence(p, c.b);
         c.blocks = blocks_of<R>(p, c.s);
         c.tiles = tiles_of(c.s);
-        c.block = static_cast<int>(left / c.tiles);
-        c.tile = static_cast<int>(left - static_cast<int64_t>(c.block) * c.tiles);
+        c.item = static_cast<int>(quotient(left, c.tiles));
+        c.tile = static_cast<int>(left - static_cast<int64_t>(c.item) * c.tiles);
+    }
+    __syncthreads();
+
+    // The next piece: tiles [c.tile, t_end) of item c.item; false at the end.
+    auto next_piece = [&](int t_end) {
+        w += t_end - c.tile;
+        c.tile = 0;
+        if (w >= w_end) return false;
+        if (++c.item >= c.blocks * head_groups) {
+            c.item = 0;
+            do {
+                if (++c.b >= p.batch) return false;
+                c.s = sequence(p, c.b);
+                c.blocks = blocks_of<R>(p, c.s);
+                c.tiles = tiles_of(c.s);
+            } while (c.blocks == 0);
+        }
+        return true;
+    };
+    auto piece_end = [&]() { return static_cast<int>(min(static_cast<int64_t>(c.tiles), c.tile + (w_end - w))); };
+    // keys that packed row pr of the sequence sees: [0, limit)
+    auto limit = [&](int pr) { return p.causal ? clampi(pr / p.group + c.s.m - c.s.n + 1, 0, c.s.m) : c.s.m; };
+    // tiles of the piece that some row sees end here
+    auto seen_end = [&](int rb, int t_end) {
+        const int last = min((rb + 1) * R, c.s.n * p.group) - 1;
+        return min(t_end, (limit(last) + kTile - 1) / kTile);
+    };
+
+    int st = 0, ph = 0;  // ring place of the next tile
+    auto next_stage = [&]() {
+        if (++st == S) {
+            st = 0;
+            ph ^= 1;
+        }
+    };
+
+    if (warp == kGroups * kWarps) {
+        // ---- producer
+        bool ok = true;
+        int loaded = 0;
+        for (bool more = true; more && ok;) {
+            const int t_end = piece_end(), hg = c.item / c.blocks, rb = c.item - hg * c.blocks;
+            const int end = seen_end(rb, t_end), hk = hg * p.side_heads + side;
+            for (int t = c.tile; t < end; ++t) {
+                ok = mbar_wait(&empty[st], ph ^ 1, 50);
+                if (!ok) break;
+                if (elect_one_sync()) {
+                    mbar_arrive_expect_tx(&full[st], L::kStage);
+                    const uint32_t dst = smem_u32(smem) + st * L::kStage;
+#pragma unroll
+                    for (int x = 0; x < DP / 64; ++x) {
+                        tma_load_3d(dst + x * L::kChunk, &tmK, &full[st], 64 * x, hk, c.s.k0 + t * kTile);
+                        tma_load_3d(dst + L::kKv + x * L::kChunk, &tmV, &full[st], 64 * x, hk, c.s.k0 + t * kTile);
+                    }
+                }
+                ++loaded;
+                next_stage();
+            }
+            more = next_piece(t_end);
+        }
+        // nothing is in flight into this CTA's shared memory when it ends: the
+        // last round of every stage that was loaded
+        for (int i = 0; i < min(S, loaded); ++i) {
+            if (--st < 0) {
+                st = S - 1;
+                ph ^= 1;
+            }
+            mbar_wait(&full[st], ph, 51);
+        }
+        return;
     }
 
-    while (w < w_end) {
-        // ---- one piece: tiles [c.tile, t_end) of row block c.block of sequence c.b
-        const int t_begin = c.tile;
-        const int t_end = static_cast<int>(min(static_cast<int64_t>(c.tiles), t_begin + (w_end - w)));
+    // ---- consumers
+    const int group = warp / kWarps, sub = warp % kWarps;
+    const int my_row = 16 * (sub % kRowTiles), my_keys = sub / kRowTiles * (kTile / kParts);  // of an item, of a tile
+    bool ok = true;
+    int turn = 0;  // group of the next tile
+    for (bool more = true; more;) {
+        const int t_begin = c.tile, t_end = piece_end();
         const int64_t item_start = w - t_begin;
-        const int rb = c.block;
+        const int hg = c.item / c.blocks, rb = c.item - hg * c.blocks, hk = hg * p.side_heads + side;
         const Sequence s = c.s;
         const int rows = min(R, s.n * p.group - rb * R);
-        const T* kbase = static_cast<const T*>(p.k) + static_cast<int64_t>(hk) * p.k_head;
-        const T* vbase = static_cast<const T*>(p.v) + static_cast<int64_t>(hk) * p.v_head;
+        const int lim_low = limit(rb * R), end = seen_end(rb, t_end);
 
-        // keys a packed row may see: [0, lim)
-        auto limit = [&](int r) {
-            if (r >= rows) return 0;
-            const int i = (rb * R + r) / p.group;
-            return p.causal ? clampi(i + s.m - s.n + 1, 0, s.m) : s.m;
-        };
-        const int lim_top = limit(rows - 1), lim_low = limit(0);
-
-        auto issue = [&](int t) {
-            const int key0 = t * kTile + warp * kKeys;
-            if (t < t_end && key0 < lim_top) {
-                uint8_t* st = pipe + ((t - t_begin) % kStages) * L::kStageBytes;
-#pragma unroll
-                for (int u = lane; u < kKeys * kChunks; u += 32) {
-                    const int r = u / kChunks, ch = u % kChunks;
-                    const int key = key0 + r;
-                    const bool take = key < lim_top && ch < dchunks;
-                    const int64_t tok = s.k0 + (take ? key : 0);
-                    const int col = take ? 8 * ch : 0;
-                    const T* ks = kbase + (take ? tok * p.k_token + col : 0);
-                    const T* vs = vbase + (take ? tok * p.v_token + col : 0);
-                    cp_async16(smem_u32(st) + swz<DP>(r, ch), ks, take);
-                    cp_async16(smem_u32(st) + kKeys * DP * 2 + swz<DP>(r, ch), vs, take);
-                }
-            }
-            cp_async_commit();
-        };
-
-        __syncthreads();  // the previous piece's join is done
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(t_begin + i);
-        // Q rows to shared memory while the first keys are on their way
-        for (int u = threadIdx.x; u < R * kChunks; u += kWarps * 32) {
+        // Q rows to shared memory
+        for (int u = threadIdx.x; u < R * kChunks; u += kConsumers) {
             const int r = u / kChunks, ch = u % kChunks;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows && ch < dchunks) {
+            if (r < rows && 8 * ch < p.D) {
                 const int pr = rb * R + r, i = pr / p.group, g = pr - i * p.group;
                 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
                                                     static_cast<int64_t>(s.q0 + i) * p.q_token +
                                                     static_cast<int64_t>(hk * p.group + g) * p.q_head + 8 * ch);
             }
-            *reinterpret_cast<uint4*>(q_smem + swz<DP>(r, ch)) = v;
+            *reinterpret_cast<uint4*>(smem + L::kQ + q_at<DP>(r, ch)) = v;
         }
-        __syncthreads();
-        uint32_t qf[kMT][DP / 16][4];
+        float o[kDT][4], mx[2], sum[2];
+        int lim[2];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+        for (int j = 0; j < kDT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk)
-                ldmatrix4(qf[mt][kk], smem_u32(q_smem) + swz<DP>(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+        for (int h = 0; h < 2; ++h) {
+            const int r = my_row + (lane >> 2) + 8 * h;
+            mx[h] = -INFINITY;
+            sum[h] = 0.0f;
+            lim[h] = r < rows ? limit(rb * R + r) : 0;
+        }
+        named_bar_sync(1, kConsumers);
+        uint32_t qf[DP / 16][4];
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+            ldmatrix4(qf[kk], smem_u32(smem) + L::kQ + q_at<DP>(my_row + (lane & 15), 2 * kk + (lane >> 4)));
 
-        float o[kMT][kDT][4], mx[kMT][2], sum[kMT][2];
-        int lim[kMT][2];
+#pragma unroll 1
+        for (int t = t_begin; t < end; ++t, turn ^= 1, next_stage()) {
+            if (turn != group) continue;
+            ok = ok && mbar_wait(&full[st], ph, 52);
+            const uint32_t ks = smem_u32(smem) + st * L::kStage, vs = ks + L::kKv;
+#pragma unroll 1
+            for (int row0 = my_keys; row0 < my_keys + kTile / kParts; row0 += kKeys) {
+                const int key0 = t * kTile + row0;
+                float sc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-            for (int j = 0; j < kDT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[mt][h] = -INFINITY;
-                sum[mt][h] = 0.0f;
-                lim[mt][h] = limit(16 * mt + (lane >> 2) + 8 * h);
-            }
-        }
-        for (int t = t_begin; t < t_end; ++t) {
-            __syncwarp();  // every lane is done with the stage that issue() refills
-            issue(t + kStages - 1);
-            cp_async_wait<kStages - 1>();
-            __syncwarp();
-            const int key0 = t * kTile + warp * kKeys;
-            if (key0 >= lim_top) continue;
-            const uint32_t ks = smem_u32(pipe + ((t - t_begin) % kStages) * L::kStageBytes);
-            const uint32_t vs = ks + kKeys * DP * 2;
-            float sc[kMT][2][4];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-                uint32_t kf[4];
-                ldmatrix4(kf, ks + swz<DP>((lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                    mma16816<T>(sc[mt][0], qf[mt][kk], kf[0], kf[1]);
-                    mma16816<T>(sc[mt][1], qf[mt][kk], kf[2], kf[3]);
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    uint32_t kf[4];
+                    ldmatrix4(kf, ks + kv_at(row0 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+                    mma16816<T>(sc[0], qf[kk], kf[0], kf[1]);
+                    mma16816<T>(sc[1], qf[kk], kf[2], kf[3]);
                 }
-            }
-            const int col = key0 + 2 * (lane & 3);
-            // A key that only some of the rows see must not reach the others
-            // through 0 * inf: such a tile with a non-finite V goes key by key.
-            bool apart = false;
-            if (key0 + kKeys > lim_low) {
-                bool bad = false;
-                for (int u = lane; u < kKeys * kChunks; u += 32) {
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "r"(vs + swz<DP>(u / kChunks, u % kChunks)));
-                    bad |= any_non_finite<T>(v);
-                }
-                apart = __any_sync(0xffffffffu, bad);
-            }
-            uint32_t pf[kMT][4];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
+                const int col = key0 + 2 * (lane & 3);
                 float tm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[mt][j][e] =
-                            col + 8 * j + (e & 1) < lim[mt][e >> 1] ? sc[mt][j][e] * p.scale_log2 : -INFINITY;
-                        tm[e >> 1] = fmaxf(tm[e >> 1], sc[mt][j][e]);
+                        sc[j][e] = col + 8 * j + (e & 1) < lim[e >> 1] ? sc[j][e] * p.scale_log2 : -INFINITY;
+                        tm[e >> 1] = fmaxf(tm[e >> 1], sc[j][e]);
                     }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 1));
                     tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 2));
                 }
-                const bool grows = tm[0] > mx[mt][0] || tm[1] > mx[mt][1];
+                const bool grows = tm[0] > mx[0] || tm[1] > mx[1];
                 if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float m = fmaxf(mx[mt][h], tm[h]);
-                        const float f = m == mx[mt][h] ? 1.0f : exp2_approx(mx[mt][h] - m);
-                        mx[mt][h] = m;
-                        sum[mt][h] *= f;
+                        const float m = fmaxf(mx[h], tm[h]);
+                        const float f = m == mx[h] ? 1.0f : exp2_approx(mx[h] - m);
+                        mx[h] = m;
+                        sum[h] *= f;
 #pragma unroll
                         for (int j = 0; j < kDT; ++j) {
-                            o[mt][j][2 * h] *= f;
-                            o[mt][j][2 * h + 1] *= f;
+                            o[j][2 * h] *= f;
+                            o[j][2 * h + 1] *= f;
                         }
                     }
                 }
-                const float base[2] = {mx[mt][0] == -INFINITY ? 0.0f : mx[mt][0],
-                                       mx[mt][1] == -INFINITY ? 0.0f : mx[mt][1]};
+                const float base[2] = {mx[0] == -INFINITY ? 0.0f : mx[0], mx[1] == -INFINITY ? 0.0f : mx[1]};
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[mt][j][e] = exp2_approx(sc[mt][j][e] - base[e >> 1]);
-                        sum[mt][e >> 1] += sc[mt][j][e];
+                        sc[j][e] = exp2_approx(sc[j][e] - base[e >> 1]);
+                        sum[e >> 1] += sc[j][e];
                     }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pf[mt][2 * j + h] = Pair16<T>::pack(sc[mt][j][2 * h], sc[mt][j][2 * h + 1]);
-            }
-            if (!apart) {
-#pragma unroll
-                for (int j = 0; j < kDT; j += 2) {
-                    uint32_t vf[4];
-                    ldmatrix4_trans(vf, vs + swz<DP>((lane & 7) + ((lane >> 3) & 1) * 8, j + (lane >> 4)));
-#pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
-                        mma16816<T>(o[mt][j], pf[mt], vf[0], vf[1]);
-                        mma16816<T>(o[mt][j + 1], pf[mt], vf[2], vf[3]);
+                // A key that only some of the rows see (or none: past the length)
+                // must not reach the others through 0 * inf: such keys with a
+                // non-finite V go one by one.
+                bool apart = false;
+                if (key0 + kKeys > lim_low) {
+                    bool bad = false;
+                    for (int u = lane; u < kKeys * kChunks; u += 32) {
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(vs + kv_at(row0 + u / kChunks, u % kChunks)));
+                        bad |= any_non_finite<T>(v);
                     }
+                    apart = __any_sync(0xffffffffu, bad);
                 }
-            } else {
+                if (!apart) {
+                    const uint32_t pf[4] = {Pair16<T>::pack(sc[0][0], sc[0][1]), Pair16<T>::pack(sc[0][2], sc[0][3]),
+                                            Pair16<T>::pack(sc[1][0], sc[1][1]), Pair16<T>::pack(sc[1][2], sc[1][3])};
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
+                    for (int j = 0; j < kDT; j += 2) {
+                        uint32_t vf[4];
+                        ldmatrix4_trans(vf, vs + kv_at(row0 + (lane & 7) + ((lane >> 3) & 1) * 8, j + (lane >> 4)));
+                        mma16816<T>(o[j], pf, vf[0], vf[1]);
+                        mma16816<T>(o[j + 1], pf, vf[2], vf[3]);
+                    }
+                } else {
 #pragma unroll 1
                     for (int k = 0; k < kKeys; ++k) {
                         // p of rows lane/4 and lane/4 + 8 at key k
                         const int from = (lane & ~3) | ((k & 7) >> 1);
                         auto pick = [&](int e) {
-                            const float even = k & 8 ? sc[mt][1][e] : sc[mt][0][e];
-                            const float odd = k & 8 ? sc[mt][1][e + 1] : sc[mt][0][e + 1];
+                            const float even = k & 8 ? sc[1][e] : sc[0][e];
+                            const float odd = k & 8 ? sc[1][e + 1] : sc[0][e + 1];
                             return __shfl_sync(0xffffffffu, k & 1 ? odd : even, from);
                         };
                         const float p0 = pick(0), p1 = pick(2);
-                        const bool s0 = key0 + k < lim[mt][0], s1 = key0 + k < lim[mt][1];
+                        const bool s0 = key0 + k < lim[0], s1 = key0 + k < lim[1];
 #pragma unroll
                         for (int j = 0; j < kDT; ++j) {
                             uint32_t w32;
                             asm volatile("ld.shared.u32 %0, [%1];"
                                          : "=r"(w32)
-                                         : "r"(vs + swz<DP>(k, j) + 4 * (lane & 3)));
+                                         : "r"(vs + kv_at(row0 + k, j) + 4 * (lane & 3)));
                             const float2 v = Pair16<T>::unpack(w32);
                             if (s0) {
-                                o[mt][j][0] = fmaf(p0, v.x, o[mt][j][0]);
-                                o[mt][j][1] = fmaf(p0, v.y, o[mt][j][1]);
+                                o[j][0] = fmaf(p0, v.x, o[j][0]);
+                                o[j][1] = fmaf(p0, v.y, o[j][1]);
                             }
                             if (s1) {
-                                o[mt][j][2] = fmaf(p1, v.x, o[mt][j][2]);
-                                o[mt][j][3] = fmaf(p1, v.y, o[mt][j][3]);
+                                o[j][2] = fmaf(p1, v.x, o[j][2]);
+                                o[j][3] = fmaf(p1, v.y, o[j][3]);
                             }
                         }
                     }
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
         }
-        cp_async_wait<0>();
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sum[mt][h] += __shfl_xor_sync(0xffffffffu, sum[mt][h], 1);
-                sum[mt][h] += __shfl_xor_sync(0xffffffffu, sum[mt][h], 2);
-            }
 
-        // ---- join the four warps
-        __syncthreads();
-        float* jm = join + warp * R * (DP + 2);
-        float* jl = jm + R;
-        float* jo = jl + R;
+        // ---- join: group 1 into group 0 (the same warp and lane hold the same
+        // rows and columns), then the parts of the keys
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+        }
+        // a warp's [16] maxima, [16] sums, [16][DP] outputs
+        constexpr int kSlot = 16 * (DP + 2);
+        float* slot = join + sub * kSlot;
+        auto put = [&]() {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = 16 * mt + 8 * h + (lane >> 2);
+                const int r = 8 * h + (lane >> 2);
                 if ((lane & 3) == 0) {
-                    jm[r] = mx[mt][h];
-                    jl[r] = sum[mt][h];
+                    slot[r] = mx[h];
+                    slot[16 + r] = sum[h];
                 }
 #pragma unroll
                 for (int j = 0; j < kDT; ++j)
-                    *reinterpret_cast<float2*>(jo + r * DP + 8 * j + 2 * (lane & 3)) =
-                        make_float2(o[mt][j][2 * h], o[mt][j][2 * h + 1]);
+                    *reinterpret_cast<float2*>(slot + 32 + r * DP + 8 * j + 2 * (lane & 3)) =
+                        make_float2(o[j][2 * h], o[j][2 * h + 1]);
             }
-        __syncthreads();
+        };
+        named_bar_sync(1, kConsumers);  // the previous item's join is done
+        if (group == 1) put();
+        named_bar_sync(1, kConsumers);
+        if (group == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * h + (lane >> 2);
+                const float m1 = slot[r], nm = fmaxf(mx[h], m1);
+                const float f0 = mx[h] == nm ? 1.0f : exp2_approx(mx[h] - nm);
+                const float f1 = m1 == nm ? 1.0f : exp2_approx(m1 - nm);
+                mx[h] = nm;
+                sum[h] = sum[h] * f0 + slot[16 + r] * f1;
+#pragma unroll
+                for (int j = 0; j < kDT; ++j) {
+                    const float2 v = *reinterpret_cast<const float2*>(slot + 32 + r * DP + 8 * j + 2 * (lane & 3));
+                    o[j][2 * h] = o[j][2 * h] * f0 + v.x * f1;
+                    o[j][2 * h + 1] = o[j][2 * h + 1] * f0 + v.y * f1;
+                }
+            }
+            __syncwarp();  // the maxima and sums of a row are read by four lanes
+            put();
+        }
+        named_bar_sync(1, kConsumers);
 
         // thread: row threadIdx.x / kPer, columns in pairs kPer apart
-        constexpr int kPer = kWarps * 32 / R, kPairs = DP / 2 / kPer;
+        constexpr int kPer = kConsumers / R, kPairs = DP / 2 / kPer;
         const int jr = threadIdx.x / kPer, jc = 2 * (threadIdx.x % kPer);
         const bool whole = t_begin == 0 && t_end == c.tiles;
         float om = -INFINITY, ol = 0.0f;
@@ -402,19 +475,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const A
         };
         clear();
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-            const float* pm = join + x * R * (DP + 2);
+        for (int x = 0; x < kParts; ++x) {
+            const float* pm = join + (x * kRowTiles + jr / 16) * kSlot;
             float2 v[kPairs];
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
-                v[i] = *reinterpret_cast<const float2*>(pm + 2 * R + jr * DP + jc + 2 * kPer * i);
-            join_into(pm[jr], pm[R + jr], v);
+                v[i] = *reinterpret_cast<const float2*>(pm + 32 + jr % 16 * DP + jc + 2 * kPer * i);
+            join_into(pm[jr % 16], pm[16 + jr % 16], v);
         }
 
         auto store = [&]() {
             if (jr >= rows) return;
             const int pr = rb * R + jr, i = pr / p.group, g = pr - i * p.group, head = hk * p.group + g;
-            const bool sees = limit(jr) > 0;
+            const bool sees = limit(pr) > 0;
             const float inv = sees ? __frcp_rn(ol) : 0.0f;  // a row that sees keys of no weight is 0 / 0
             T* dst = static_cast<T*>(p.o) + static_cast<int64_t>(s.q0 + i) * p.o_token +
                      static_cast<int64_t>(head) * p.o_head;
@@ -443,19 +516,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const A
             for (int i = 0; i < kPairs; ++i)
                 *reinterpret_cast<float2*>(part + 2 * R + jr * DP + jc + 2 * kPer * i) = ov[i];
             __threadfence();
-            __syncthreads();
-            const int first = static_cast<int>(item_start / per);
-            const int last = static_cast<int>((item_start + c.tiles - 1) / per);
-            int* counter = p.counters + first * p.Hk + hk;
+            named_bar_sync(1, kConsumers);
+            const int first = static_cast<int>(quotient(item_start, per));
+            const int last = static_cast<int>(quotient(item_start + c.tiles - 1, per));
+            int* counter = p.counters + first * p.side_heads + side;
             if (threadIdx.x == 0) last_flag = atomicAdd(counter, 1) == last - first;
-            __syncthreads();
+            named_bar_sync(1, kConsumers);
             if (last_flag) {
                 __threadfence();
                 clear();
 #pragma unroll (R == 16 ? 4 : 1)
                 for (int x = first; x <= last; ++x) {
                     // the first piece starts at the item's tile 0
-                    const float* src = p.partial + (2 * (static_cast<int64_t>(x) * p.Hk + hk) + (x == first)) * kPart;
+                    const float* src =
+                        p.partial + (2 * (static_cast<int64_t>(x) * p.side_heads + side) + (x == first)) * kPart;
                     float2 v[kPairs];
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i)
@@ -466,24 +540,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_split_kernel(const A
                 if (threadIdx.x == 0) *counter = 0;  // ready for the next call
             }
         }
-
-        // ---- next row block
-        w += t_end - t_begin;
-        c.tile = 0;
-        if (++c.block >= c.blocks) {
-            c.block = 0;
-            do {
-                if (++c.b >= p.batch) return;
-                c.s = sequence(p, c.b);
-                c.blocks = blocks_of<R>(p, c.s);
-                c.tiles = tiles_of(c.s);
-            } while (c.blocks == 0);
-        }
+        more = next_piece(t_end);
     }
 }
 
 template <typename T, int DP, int R>
-cudaError_t launch_split_rows(const AttentionArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_split_rows(const CUtensorMap (&map)[2], const AttentionArgs& a, int ctas, cudaStream_t st) {
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -494,39 +556,97 @@ cudaError_t launch_split_rows(const AttentionArgs& a, int ctas, cudaStream_t st)
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
-    attention_split_kernel<T, DP, R><<<ctas, kWarps * 32, SplitSmem<DP, R>::kTotal, st>>>(a);
+    attention_split_kernel<T, DP, R><<<ctas, kConsumers + 32, SplitSmem<DP, R>::kTotal, st>>>(map[0], map[1], a);
     return cudaGetLastError();
 }
 
 template <typename T, int DP>
-cudaError_t launch_split(const AttentionArgs& a, int ctas, cudaStream_t st) {
-    // two MMA tiles of rows where a sequence has more than 16: its keys are read half as often
-    return static_cast<int64_t>(a.Tq) * a.group > 16 * static_cast<int64_t>(a.batch)
-               ? launch_split_rows<T, DP, 32>(a, ctas, st)
-               : launch_split_rows<T, DP, 16>(a, ctas, st);
+cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, int ctas, cudaStream_t st) {
+    // as many rows an item as a sequence has, so that its keys are read once
+    const int64_t rows = static_cast<int64_t>(a.Tq) * a.group;
+    if (rows <= 16 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 16>(map, a, ctas, st);
+    if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32>(map, a, ctas, st);
+    return launch_split_rows<T, DP, 64>(map, a, ctas, st);
 }
 
-// Two CTAs per SM, a whole number of key ranges (one at least) for all KV heads.
-int split_ctas(int num_sms, int Hk) { return 2 * num_sms / Hk > 0 ? 2 * num_sms / Hk * Hk : Hk; }
+// Heads that run side by side: the largest divisor of Hk up to 8.
+int side_heads(int Hk) {
+    for (int h = 8; h > 1; --h)
+        if (Hk % h == 0) return h;
+    return 1;
+}
 
 }  // namespace
 
-size_t attention_counter_bytes(int num_sms) { return (static_cast<size_t>(2 * num_sms) * 4 + 255) / 256 * 256; }
+size_t attention_counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 4 + 255) / 256 * 256; }
 
 size_t attention_workspace_bytes(int num_sms) {
-    return attention_counter_bytes(num_sms) + static_cast<size_t>(2 * num_sms) * 2 * kPartFloats<128, 32> * 4;
+    return attention_counter_bytes(num_sms) + static_cast<size_t>(num_sms) * 2 * kPartFloats<128, 64> * 4;
 }
 
-cudaError_t launch_attention(const AttentionArgs& args, int dtype, int num_sms, void* workspace, cudaStream_t st) {
+// Whether to split the keys over the CTAs rather than run the prompt kernel:
+// always up to one MMA tile of rows per sequence (the keys' bytes bound it);
+// above, by what a key costs.  The prompt kernel takes 7 ns a key for each wave
+// of items (a pair of 128-row tiles per SM), the split kernel 0.13 ns for each
+// block of 64 rows, and 2 us more around them.  Measured at 40 query heads on 8
+// KV heads x 128: 1 sequence x 64 queries over 32768 keys 198 us split against
+// 356, 4 x 8 over 32768 165 against 242, 4 x 16 289 against 242, 16 x 8 over
+// 4096 98 against 54, 1 x 4 over 512 15.2 against 13.6.
+bool attention_splits(const AttentionArgs& a, int num_sms) {
+    const int64_t rows = static_cast<int64_t>(a.Tq) * a.group, batch = a.batch;
+    if (rows <= 16 * batch) return true;
+    if (a.group > 128 || a.Tk < 1024 * batch) return a.group > 128;
+    const int64_t blocks = (rows + 64 * batch - 1) / (64 * batch) * batch * a.Hk;
+    const int64_t tokens = 2 * (128 / a.group);  // of an item of the prompt kernel
+    const int64_t items = (a.Tq + tokens * batch - 1) / (tokens * batch) * batch * a.Hk;
+    return blocks < 54 * ((items + num_sms - 1) / num_sms);
+}
+
+cudaError_t encode_heads(void* encode_fn, CUtensorMap* map, char name, const void* ptr, int dtype, int rows, int heads,
+                         int dim, int64_t token, int64_t head, int box_heads, int box_rows, char* detail, size_t n) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode_fn)(
+        map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+        const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return cudaSuccess;
+    snprintf(detail, n, "cuTensorMapEncodeTiled(%c: %d x %d x %d) returned %d", name, rows, heads, dim,
+             static_cast<int>(r));
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num_sms, void* workspace, void* encode_fn,
+                                   cudaStream_t st, char* detail, size_t n) {
     AttentionArgs a = args;
     a.counters = static_cast<int*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attention_counter_bytes(num_sms));
-    a.min_tiles = 2;
-    // (with more KV heads than CTAs there is one range: no piece, no partial result)
-    const int ctas = split_ctas(num_sms, a.Hk);
+    a.side_heads = side_heads(a.Hk);
+    CUtensorMap map[2] = {};  // without keys, nothing is loaded
+    if (a.Tk > 0) {
+        cudaError_t e = encode_heads(encode_fn, &map[0], 'K', a.k, dtype, a.Tk, a.Hk, a.D, a.k_token, a.k_head, 1,
+                                     kTile, detail, n);
+        if (e == cudaSuccess)
+            e = encode_heads(encode_fn, &map[1], 'V', a.v, dtype, a.Tk, a.Hk, a.D, a.v_token, a.v_head, 1, kTile,
+                             detail, n);
+        if (e != cudaSuccess) return e;
+    }
+    const int ctas = num_sms / a.side_heads * a.side_heads;
     if (dtype == kBf16)
-        return a.D <= 64 ? launch_split<__nv_bfloat16, 64>(a, ctas, st) : launch_split<__nv_bfloat16, 128>(a, ctas, st);
-    return a.D <= 64 ? launch_split<__half, 64>(a, ctas, st) : launch_split<__half, 128>(a, ctas, st);
+        return a.D <= 64 ? launch_split<__nv_bfloat16, 64>(map, a, ctas, st)
+                         : launch_split<__nv_bfloat16, 128>(map, a, ctas, st);
+    return a.D <= 64 ? launch_split<__half, 64>(map, a, ctas, st) : launch_split<__half, 128>(map, a, ctas, st);
+}
+
+cudaError_t attention_split_read_device_error(unsigned int* code) {
+    unsigned int v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
+    *code = v;
+    return e;
 }
 
 }  // namespace w8a8

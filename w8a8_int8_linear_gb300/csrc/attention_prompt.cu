@@ -42,7 +42,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cstdio>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -100,15 +99,6 @@ struct Bars {
     Item items[2];
 };
 static_assert(sizeof(Bars) <= 768, "barriers fit their room");
-
-__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
-                                            int32_t c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
 
 // Shared-memory operand descriptors with the 128-byte swizzle, low words built
 // from an address by adding (address >> 4); the high word is the same for all:
@@ -693,42 +683,21 @@ int64_t most_items(const AttentionArgs& a) {
 
 }  // namespace
 
-bool attention_prompt_takes(const AttentionArgs& a) {
-    // TMA strides are positive and below 2^40 bytes
-    const int64_t s[6] = {a.q_token, a.q_head, a.k_token, a.k_head, a.v_token, a.v_head};
-    for (int64_t v : s)
-        if (v <= 0 || v >= int64_t(1) << 39) return false;
-    return a.Tk > 0 && a.group <= kTileRows && most_items(a) <= INT32_MAX / 2;
-}
-
 cudaError_t launch_attention_prompt(const AttentionArgs& args, int dtype, int num_sms, void* workspace,
                                     void* encode_fn, cudaStream_t st, char* detail, size_t n) {
     AttentionArgs a = args;
     a.counters = static_cast<int*>(workspace);
-    auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode_fn);
     CUtensorMap map[3];
-    for (int i = 0; i < 3; ++i) {
-        const void* ptr = i == 0 ? a.q : i == 1 ? a.k : a.v;
-        const int64_t token = i == 0 ? a.q_token : i == 1 ? a.k_token : a.v_token;
-        const int64_t head = i == 0 ? a.q_head : i == 1 ? a.k_head : a.v_head;
-        const int heads = i == 0 ? a.Hq : a.Hk, rows = i == 0 ? a.Tq : a.Tk;
-        cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(heads),
-                              static_cast<cuuint64_t>(rows)};
-        cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2};
-        cuuint32_t box[3] = {64, i == 0 ? static_cast<cuuint32_t>(a.group) : 1u,
-                             i == 0 ? static_cast<cuuint32_t>(kTileRows / a.group) : static_cast<cuuint32_t>(kKeyTile)};
-        cuuint32_t estr[3] = {1, 1, 1};
-        const CUresult r = encode(&map[i],
-                                  dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS) {
-            snprintf(detail, n, "cuTensorMapEncodeTiled(%c: %d x %d x %d) returned %d", "QKV"[i], rows, heads, a.D,
-                     static_cast<int>(r));
-            return cudaErrorInvalidValue;
-        }
-    }
+    constexpr int kKeyBox = kKeyTile;
+    cudaError_t e = encode_heads(encode_fn, &map[0], 'Q', a.q, dtype, a.Tq, a.Hq, a.D, a.q_token, a.q_head, a.group,
+                                 kTileRows / a.group, detail, n);
+    if (e == cudaSuccess)
+        e = encode_heads(encode_fn, &map[1], 'K', a.k, dtype, a.Tk, a.Hk, a.D, a.k_token, a.k_head, 1, kKeyBox, detail,
+                         n);
+    if (e == cudaSuccess)
+        e = encode_heads(encode_fn, &map[2], 'V', a.v, dtype, a.Tk, a.Hk, a.D, a.v_token, a.v_head, 1, kKeyBox, detail,
+                         n);
+    if (e != cudaSuccess) return e;
     const int64_t items = most_items(a);
     const int grid = items < num_sms ? static_cast<int>(items) : num_sms;
     if (dtype == kBf16)

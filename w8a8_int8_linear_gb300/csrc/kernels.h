@@ -108,23 +108,30 @@ struct AttentionArgs {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
     float scale_log2;       // scale * log2(e)
     int causal;
-    // filled in by launch_attention
+    // filled in by the launchers
     int* counters;
     float* partial;
-    int min_tiles;
+    int side_heads;
 };
 size_t attention_workspace_bytes(int num_sms);
 // The workspace's counters (its first attention_counter_bytes) are zero
 // before the first call; every call leaves them zero.
 size_t attention_counter_bytes(int num_sms);
-cudaError_t launch_attention(const AttentionArgs& a, int dtype, int num_sms, void* workspace, cudaStream_t st);
-// The tensor-core kernel for many queries per sequence, on the calls it
-// takes; `encode_fn` is the driver's cuTensorMapEncodeTiled.  On failure a
-// one-line description is written to `detail` (size `n`).
-bool attention_prompt_takes(const AttentionArgs& a);
+// Two kernels: for few queries per sequence, with the keys split over the CTAs,
+// and for many on the tensor cores (attention_splits says which).  `encode_fn` is the
+// driver's cuTensorMapEncodeTiled.  On failure a one-line description may be
+// written to `detail` (size `n`).
+cudaError_t launch_attention_split(const AttentionArgs& a, int dtype, int num_sms, void* workspace, void* encode_fn,
+                                   cudaStream_t st, char* detail, size_t n);
+bool attention_splits(const AttentionArgs& a, int num_sms);
 cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, int num_sms, void* workspace, void* encode_fn,
                                     cudaStream_t st, char* detail, size_t n);
+// Tensor map of [rows, heads, dim] 16-bit elements (strides in elements) with
+// boxes of 64 x box_heads x box_rows, 128-byte swizzled; elements outside are 0.
+cudaError_t encode_heads(void* encode_fn, CUtensorMap* map, char name, const void* ptr, int dtype, int rows, int heads,
+                         int dim, int64_t token, int64_t head, int box_heads, int box_rows, char* detail, size_t n);
 cudaError_t attention_read_device_error(unsigned int* code);
+cudaError_t attention_split_read_device_error(unsigned int* code);
 
 // One [rows, heads, dim] side of the rotary kernel; strides count elements.
 struct Heads {

@@ -93,6 +93,10 @@ def attention(Q, K, V, cu_q=None, cu_k=None, k_lens=None, batch=1, causal=True, 
     dtype, device = Q.dtype, Q.device
     k_token, k_head = _heads(K, "K", dtype)
     v_token, v_head = _heads(V, "V", dtype)
+    if not (q_token and q_head and k_token and k_head and v_token and v_head):
+        # a broadcast dimension is laid out
+        Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+        (q_token, q_head), (k_token, k_head), (v_token, v_head) = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V")
     tq, hq, d = Q.shape
     tk, hk, dk = K.shape
     if dk != d or V.shape != K.shape:
