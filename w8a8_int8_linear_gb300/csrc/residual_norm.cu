@@ -11,17 +11,21 @@
 //   n  = (h - mu) / sqrt(S((h - mu)^2)/K + eps) * gamma + beta
 //                                                     (mu = 0 for RMSNorm)
 //   y  = n * (1 + mod_scale) + mod_shift
-//   sx = max|y| / 127, code = clamp(rne(y * (1/sx)), -127, 127)
+//   sx = max|y| / 127, code = rne(y * (1/sx))
 //
 // Everything between the loads and the stores is binary32: the norm goes on
 // from the unrounded h, and the quantization takes the unrounded y (rounding
 // either to bf16 first would only add its half step, 2^-8, to the error).
 //
+// With r the reciprocal root and v = (h - mu) * gamma, y = v * r where nothing
+// else is asked for, and max|y| = r * max|v|: the sum of squares and the maximum
+// then go through one reduction over the CTA.
+//
 // Bytes bound it (read x and b, write h and y or the image: 8 bytes an
-// element), and a row passes two to four reductions over the CTA between its
-// loads and its stores.  With many rows a CTA therefore takes rows in a loop
-// and bulk copies keep its next rows on the way to shared memory while it
-// works on the present one; with few rows each CTA loads its row directly.
+// element), and a row passes one to four reductions between its loads and its
+// stores.  With many rows a CTA therefore takes rows in a loop and bulk copies
+// keep its next rows on the way to shared memory while it works on the present
+// one; with few rows each CTA loads its row directly.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,37 +47,26 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+__device__ __forceinline__ float warp_max_abs(float v) {
+    float m;
+    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
-// Sum (or maximum) over the CTA; every thread gets it.  `red` is this
-// reduction's own scratch, so one barrier suffices; the order is fixed.
-template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float* red) {
+// Sum of a (kSum) and maximum of |b| (kMax) over the CTA; every thread gets
+// both.  `red` is this reduction's own scratch, so one barrier suffices; the
+// order is fixed.
+template <bool kSum, bool kMax>
+__device__ __forceinline__ float2 block_reduce(float a, float b, float2* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    v = kMax ? warp_max(v) : warp_sum(v);
-    if (lane == 0) red[warp] = v;
+    if (kSum) a = warp_sum(a);
+    if (kMax) b = warp_max_abs(b);
+    if (lane == 0) red[warp] = make_float2(a, b);
     __syncthreads();
-    v = lane < warps ? red[lane] : 0.0f;
-    return kMax ? warp_max(v) : warp_sum(v);
-}
-
-__device__ __forceinline__ void load8(const void* base, int64_t chunk, float (&v)[8]) {
-    const uint4 w = __ldg(static_cast<const uint4*>(base) + chunk);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = P16::unpack(u[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(P16::pack(v[0], v[1]), P16::pack(v[2], v[3]), P16::pack(v[4], v[5]), P16::pack(v[6], v[7]));
+    float2 v = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+    if (kSum) v.x = warp_sum(v.x);
+    if (kMax) v.y = warp_max_abs(v.y);
+    return v;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
@@ -85,6 +78,13 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
         v[2 * i + 1] = f.y;
     }
 }
+__device__ __forceinline__ void load8(const void* base, int64_t chunk, float (&v)[8]) {
+    unpack8(__ldg(static_cast<const uint4*>(base) + chunk), v);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(P16::pack(v[0], v[1]), P16::pack(v[2], v[3]), P16::pack(v[4], v[5]), P16::pack(v[6], v[7]));
+}
 
 constexpr int kMaxStages = 4;
 constexpr int kRingBytes = 200 * 1024;
@@ -92,10 +92,17 @@ constexpr int kRingBytes = 200 * 1024;
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...: C chunks of 8 elements per
 // thread, chunk threadIdx.x + i * blockDim.x.  kRing: rows come through
 // `stages` shared-memory buffers (x, then b), else straight from memory.
-template <int C, bool kF32, bool kRing>
-__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNormArgs p, int stages) {
+// kOptions: with a branch norm, gate, modulation or beta; without, the code
+// for them does not cost the common form its registers.
+template <int C, bool kF32, bool kRing, bool kOptions>
+__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNormArgs args, int stages) {
+    ResidualNormArgs p = args;
+    if (!kOptions) {
+        p.branch_gamma = p.beta = p.gate = p.mod_scale = p.mod_shift = nullptr;
+        p.rows_per_group = 0;
+    }
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][4][32];
+    __shared__ float2 red[2][4][32];
     __shared__ uint64_t full[kMaxStages];
     constexpr int kXBytes = kF32 ? 4 : 2;
     const int chunks = static_cast<int>(p.K >> 3);
@@ -125,7 +132,6 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
         const int64_t base = row * chunks;
         const int64_t group = p.rows_per_group ? row / p.rows_per_group : 0;
         const int64_t mod = group * (p.mod_stride >> 3);
-        float h[C][8], x[C][8];
         if (kRing && !mbar_wait(&full[st], phase, 80)) {
             // recorded; the copies still on their way land before the CTA ends
             if (threadIdx.x == 0)
@@ -137,28 +143,21 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
             return;
         }
         const uint8_t* buf = ring + static_cast<size_t>(st) * (x_bytes + b_bytes);
+        // x not through the read-only path: H may be X itself
+        const uint4* xs = kRing ? reinterpret_cast<const uint4*>(buf)
+                                : reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.X) + row * x_bytes);
+        const uint4* bs = kRing ? reinterpret_cast<const uint4*>(buf + x_bytes)
+                                : reinterpret_cast<const uint4*>(p.B) + base;
+        constexpr int kX = kF32 ? 2 : 1;
+        uint4 xw[C][kX], bw[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
+            bw[i] = c < chunks ? bs[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = x[i][j] = 0.0f;
-            if (c >= chunks) continue;
-            // x not through the read-only path: H may be X itself
-            const uint4* xs = kRing ? reinterpret_cast<const uint4*>(buf)
-                                    : reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.X) + row * x_bytes);
-            const uint4* bs = kRing ? reinterpret_cast<const uint4*>(buf + x_bytes)
-                                    : reinterpret_cast<const uint4*>(p.B) + base;
-            if (kF32) {
-                const uint4 u = xs[2 * c], w = xs[2 * c + 1];
-                x[i][0] = __uint_as_float(u.x); x[i][1] = __uint_as_float(u.y);
-                x[i][2] = __uint_as_float(u.z); x[i][3] = __uint_as_float(u.w);
-                x[i][4] = __uint_as_float(w.x); x[i][5] = __uint_as_float(w.y);
-                x[i][6] = __uint_as_float(w.z); x[i][7] = __uint_as_float(w.w);
-            } else {
-                unpack8(xs[c], x[i]);
-            }
-            unpack8(bs[c], h[i]);
+            for (int k = 0; k < kX; ++k) xw[i][k] = c < chunks ? xs[kX * c + k] : make_uint4(0, 0, 0, 0);
         }
+        float h[C][8];
         bool fetched = !kRing;
         // after the first reduction's barrier every thread has read its part of
         // the buffer: the row that goes there next can be fetched
@@ -169,44 +168,54 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
             }
             fetched = true;
         };
+        float branch = 1.0f;  // reciprocal root of the branch's mean square
         if (p.branch_gamma) {
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < C; ++i)
+            for (int i = 0; i < C; ++i) {
+                unpack8(bw[i], h[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
-            const float r = __frcp_rn(__fsqrt_rn(fmaf(block_reduce<false>(s, red[odd][0]), inv_k, p.eps)));
-            refill();
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const int c = threadIdx.x + i * blockDim.x;
-                if (c >= chunks) continue;
-                float g[8];
-                load8(p.branch_gamma, c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * r * g[j];
             }
+            branch = __frcp_rn(__fsqrt_rn(fmaf(block_reduce<true, false>(s, 0.0f, red[odd][0]).x, inv_k, p.eps)));
+            refill();
         }
-        float s = 0.0f;
+        // h; RMSNorm's v right away
+        auto scaled = [&](int c, float(&v)[8]) {  // d -> v
+            if (!p.gamma) return;
+            float g[8];
+            load8(p.gamma, c, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= g[j];
+        };
+        float s = 0.0f, top = 0.0f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= chunks) continue;
+            unpack8(bw[i], h[i]);
+            float g[8];
+            if (p.branch_gamma) {
+                load8(p.branch_gamma, c, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * branch * g[j];
+            }
             if (p.gate) {
-                float g[8];
                 load8(p.gate, mod + c, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * g[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = fmaf(p.alpha, x[i][j], h[i][j]);
-            if (p.layer) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s += h[i][j];
+            if (kF32) {
+                const uint4 u = xw[i][0], v = xw[i][kX - 1];
+                g[0] = __uint_as_float(u.x); g[1] = __uint_as_float(u.y);
+                g[2] = __uint_as_float(u.z); g[3] = __uint_as_float(u.w);
+                g[4] = __uint_as_float(v.x); g[5] = __uint_as_float(v.y);
+                g[6] = __uint_as_float(v.z); g[7] = __uint_as_float(v.w);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+                unpack8(xw[i][0], g);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] = fmaf(p.alpha, g[j], h[i][j]);
             if (kF32) {
                 float4* d = static_cast<float4*>(p.H) + 2 * (base + c);
                 d[0] = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
@@ -214,90 +223,127 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
             } else {
                 static_cast<uint4*>(p.H)[base + c] = pack8(h[i]);
             }
+            if (p.layer) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += h[i][j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+                if (!kOptions) {
+                    scaled(c, h[i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                }
+            }
         }
-        s = block_reduce<false>(s, red[odd][1]);
+        float2 all = p.layer || kOptions ? block_reduce<true, false>(s, 0.0f, red[odd][1])
+                                         : block_reduce<true, true>(s, top, red[odd][1]);
         refill();
-        float mu = 0.0f;
         if (p.layer) {  // the variance about the mean, from the values in registers
-            mu = s * inv_k;
+            const float mu = all.x * inv_k;
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                if (static_cast<int>(threadIdx.x + i * blockDim.x) >= chunks) continue;
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c >= chunks) continue;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(h[i][j] - mu, h[i][j] - mu, s);
+                for (int j = 0; j < 8; ++j) {
+                    h[i][j] -= mu;
+                    s = fmaf(h[i][j], h[i][j], s);
+                }
+                if (!kOptions) {
+                    scaled(c, h[i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                }
             }
-            s = block_reduce<false>(s, red[odd][2]);
-        }
-        const float r = __frcp_rn(__fsqrt_rn(fmaf(s, inv_k, p.eps)));
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c >= chunks) continue;
-            float g[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = (h[i][j] - mu) * r;
-            if (p.gamma) {
-                load8(p.gamma, c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
-            }
-            if (p.beta) {
-                load8(p.beta, c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] += g[j];
-            }
-            if (p.mod_scale) {
-                load8(p.mod_scale, mod + c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j], g[j], h[i][j]);
-            }
-            if (p.mod_shift) {
-                load8(p.mod_shift, mod + c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] += g[j];
-            }
-            if (p.Y) static_cast<uint4*>(p.Y)[base + c] = pack8(h[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+            all = block_reduce<true, !kOptions>(s, top, red[odd][2]);
         }
         if (kRing && ++st == stages) {
             st = 0;
             phase ^= 1;
         }
+        const float r = __frcp_rn(__fsqrt_rn(fmaf(all.x, inv_k, p.eps)));
+        float peak = all.y * r;
+        if (kOptions) {
+            top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c >= chunks) continue;
+                float g[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] *= r;
+                scaled(c, h[i]);
+                if (p.beta) {
+                    load8(p.beta, c, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[i][j] += g[j];
+                }
+                if (p.mod_scale) {
+                    load8(p.mod_scale, mod + c, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j], g[j], h[i][j]);
+                }
+                if (p.mod_shift) {
+                    load8(p.mod_shift, mod + c, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[i][j] += g[j];
+                }
+                if (p.sx) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                }
+            }
+            if (p.sx) peak = block_reduce<false, true>(0.0f, top, red[odd][3]).y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] *= r;
+        }
+        if (p.Y) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c < chunks) static_cast<uint4*>(p.Y)[base + c] = pack8(h[i]);
+            }
+        }
         if (!p.sx) continue;
-        const RowScale sc = make_scale_div(block_reduce<true>(top, red[odd][3]));
+        const RowScale sc = make_scale_div(peak);
         if (threadIdx.x == 0) p.sx[row] = sc.s;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= chunks) continue;
+            // rne(y / sx) + 1.5 * 2^23, the code in the low byte; never above 127, as
+            // max|y| / sx is within a few roundings of 127
             float q[8];
             if (sc.exact) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(quant_exact(h[i][j], sc.s));
+                for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(quant_exact(h[i][j], sc.s)) + kRoundMagic;
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(rintf(h[i][j] * sc.inv), -kQMax), kQMax);
+                for (int j = 0; j < 8; ++j) q[j] = fmaf(h[i][j], sc.inv, kRoundMagic);
+            }
+            if (p.Xq) {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(q[j]);
+                reinterpret_cast<uint2*>(p.Xq)[base + c] = make_uint2(
+                    __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
             }
             if (p.Ximg) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] += 0.0f;  // the code 0 has one image, +0
+                for (int j = 0; j < 8; ++j) q[j] -= kRoundMagic;  // the code 0 is +0
                 static_cast<uint4*>(p.Ximg)[base + c] = pack8(q);
-            }
-            if (p.Xq) {
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j >> 2] |= (static_cast<uint32_t>(static_cast<int>(q[j])) & 0xFFu) << (8 * (j & 3));
-                reinterpret_cast<uint2*>(p.Xq)[base + c] = make_uint2(w[0], w[1]);
             }
         }
     }
 }
 
-template <int C, bool kF32>
+template <int C, bool kF32, bool kOptions>
 cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st) {
     const int chunks = static_cast<int>(a.K >> 3);
     const int threads = 32 * ((chunks + 32 * C - 1) / (32 * C));
@@ -305,34 +351,40 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st)
     // CTAs that fit an SM by their threads (64 registers each), and two to four
     // row buffers for each in 200 KB
     int per_sm = 1024 / threads;
-    if (per_sm > 6) per_sm = 6;
+    if (per_sm > 8) per_sm = 8;
     while (per_sm > 1 && per_sm * 2 * row_bytes > kRingBytes) --per_sm;
     int stages = kRingBytes / (per_sm * row_bytes);
-    if (stages > 4) stages = 4;
+    if (stages > kMaxStages) stages = kMaxStages;
     if (a.M <= static_cast<int64_t>(num_sms) * per_sm) {
-        residual_norm_kernel<C, kF32, false><<<static_cast<unsigned>(a.M), threads, 0, st>>>(a, 0);
+        residual_norm_kernel<C, kF32, false, kOptions><<<static_cast<unsigned>(a.M), threads, 0, st>>>(a, 0);
         return cudaGetLastError();
     }
-    const size_t smem = static_cast<size_t>(stages) * row_bytes;
-    static int allowed[64] = {};
+    static bool allowed[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || allowed[dev] == 0) {
-        e = cudaFuncSetAttribute(residual_norm_kernel<C, kF32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 208 * 1024);
+    if (dev >= 64 || !allowed[dev]) {
+        e = cudaFuncSetAttribute(residual_norm_kernel<C, kF32, true, kOptions>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
         if (e != cudaSuccess) return e;
-        if (dev < 64) allowed[dev] = 1;
+        if (dev < 64) allowed[dev] = true;
     }
-    residual_norm_kernel<C, kF32, true><<<num_sms * per_sm, threads, smem, st>>>(a, stages);
+    residual_norm_kernel<C, kF32, true, kOptions>
+        <<<num_sms * per_sm, threads, static_cast<size_t>(stages) * row_bytes, st>>>(a, stages);
     return cudaGetLastError();
+}
+
+template <bool kF32, bool kOptions>
+cudaError_t launch_width(const ResidualNormArgs& a, int num_sms, cudaStream_t st) {
+    return a.K <= 2048 ? launch_rows<1, kF32, kOptions>(a, num_sms, st) : launch_rows<2, kF32, kOptions>(a, num_sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool f32, int num_sms, cudaStream_t st) {
-    if (a.K <= 2048) return f32 ? launch_rows<1, true>(a, num_sms, st) : launch_rows<1, false>(a, num_sms, st);
-    return f32 ? launch_rows<2, true>(a, num_sms, st) : launch_rows<2, false>(a, num_sms, st);
+    const bool options = a.branch_gamma || a.beta || a.gate || a.mod_scale || a.mod_shift;
+    if (f32) return options ? launch_width<true, true>(a, num_sms, st) : launch_width<true, false>(a, num_sms, st);
+    return options ? launch_width<false, true>(a, num_sms, st) : launch_width<false, false>(a, num_sms, st);
 }
 
 cudaError_t residual_norm_read_device_error(unsigned int* code) {
