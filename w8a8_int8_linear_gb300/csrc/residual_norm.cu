@@ -86,7 +86,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(P16::pack(v[0], v[1]), P16::pack(v[2], v[3]), P16::pack(v[4], v[5]), P16::pack(v[6], v[7]));
 }
 
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
 constexpr int kRingBytes = 200 * 1024;
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...: C chunks of 8 elements per
@@ -348,13 +348,20 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st)
     const int chunks = static_cast<int>(a.K >> 3);
     const int threads = 32 * ((chunks + 32 * C - 1) / (32 * C));
     const int row_bytes = static_cast<int>(a.K) * (kF32 ? 6 : 4);
-    // CTAs that fit an SM by their threads (64 registers each), and two to four
-    // row buffers for each in 200 KB
-    int per_sm = 1024 / threads;
+    // Fewer rows in flight are better where little is computed between load and
+    // store, more where a row passes several reductions.  Measured, CTAs x buffers:
+    // 32768 x 5120 to the image 209 us at 2 x 3 (228 at 3 x 2, 235 at 4 x 2), 32768
+    // x 4096 166 at 3 x 3 (189 at 4 x 2), x 8192 321 at 2 x 3 (356 at 3 x 2); with
+    // gate, scale and shift over fp32 16384 x 5120 198 at 3 x 2 (219 at 2 x 3),
+    // 4096 x 4096 46 at 4 x 2 (60 at 2 x 3).  So too where an SM has few rows to
+    // share out: 4096 x 4096 to the image 22.8 at 4 x 2 (25.5 at 3 x 3).
+    const bool many = kOptions || a.M < static_cast<int64_t>(num_sms) * 32;
+    int per_sm = many ? 1024 / threads : (768 + threads / 2) / threads;
     if (per_sm > 8) per_sm = 8;
-    while (per_sm > 1 && per_sm * 2 * row_bytes > kRingBytes) --per_sm;
-    int stages = kRingBytes / (per_sm * row_bytes);
-    if (stages > kMaxStages) stages = kMaxStages;
+    if (per_sm < 1) per_sm = 1;
+    int stages = many ? 2 : 3;
+    while (per_sm > 1 && per_sm * stages * row_bytes > kRingBytes) --per_sm;
+    if (stages * row_bytes > kRingBytes) stages = 2;
     if (a.M <= static_cast<int64_t>(num_sms) * per_sm) {
         residual_norm_kernel<C, kF32, false, kOptions><<<static_cast<unsigned>(a.M), threads, 0, st>>>(a, 0);
         return cudaGetLastError();
