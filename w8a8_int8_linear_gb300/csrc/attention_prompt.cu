@@ -167,43 +167,100 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Item `index`, by one warp.  A sequence's items run from its last rows (the
-// most keys) to its first, KV heads innermost.
-__device__ __forceinline__ Item find_item(const AttentionArgs& p, int index, int tile_tokens) {
-    const int lane = threadIdx.x & 31;
-    Item it{};
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        int mine = 0;
-        if (b0 + lane < p.batch) mine = (sequence(p, b0 + lane).n + 2 * tile_tokens - 1) / (2 * tile_tokens) * p.Hk;
-        int incl = mine;
+// The items of a call, by one warp.  They go through the sequences, those with
+// the most keys first (up to 32 sequences), each from its last rows (the most
+// keys) to its first, KV heads innermost, two tiles an item.  Full attention
+// has items of one size: what is left over from whole rounds of CTAs, if its
+// tiles fit one round, is taken apart into them (a tile alone takes 0.6 to 0.7
+// of an item's time): 16384 queries x 8 heads 717 -> 650 us, 4096 x 32 193 ->
+// 180.  Causal items end short, and there this costs 1 to 3%.
+struct Items {
+    int sequence_of;  // of this lane, in order
+    int mine, incl;   // items of this lane's sequence, and of all up to it
+    int all;          // pairs of tiles
+    int apart, until; // those from `apart` to `until` are taken apart
+    int tile_tokens, key_tile;
+
+    // items of sequences b0 .. b0 + 31 (in order for b0 = 0)
+    __device__ __forceinline__ void count(const AttentionArgs& p, int b0, int b) {
+        const int lane = threadIdx.x & 31;
+        mine = b0 + lane < p.batch ? (sequence(p, b).n + 2 * tile_tokens - 1) / (2 * tile_tokens) * p.Hk : 0;
+        incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int t = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += t;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, incl > index);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            const int local = index - __shfl_sync(0xffffffffu, incl - mine, l);
-            const int blocks = __shfl_sync(0xffffffffu, mine, l) / p.Hk;
-            const Sequence s = sequence(p, b0 + l);
-            it.any = 1;
-            it.q0 = s.q0;
-            it.n = s.n;
-            it.k0 = s.k0;
-            it.m = s.m;
-            it.hk = local % p.Hk;
-            it.token0 = (blocks - 1 - local / p.Hk) * 2 * tile_tokens;
-            auto limit = [&](int token) { return p.causal ? clampi(token + s.m - s.n + 1, 0, s.m) : s.m; };
-            it.tiles = it.token0 + tile_tokens < s.n ? 2 : 1;
-            it.keys = (limit(min(it.token0 + 2 * tile_tokens, s.n) - 1) + kKeyTile - 1) / kKeyTile;
-            it.edge = limit(it.token0) / kKeyTile;
-            return it;
-        }
-        index -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    return it;
-}
+
+    __device__ __forceinline__ void start(const AttentionArgs& p, int tokens, int keys) {
+        const int lane = threadIdx.x & 31;
+        tile_tokens = tokens;
+        key_tile = keys;
+        sequence_of = lane;
+        if (p.batch > 1 && p.batch <= 32) {
+            // place of this lane's sequence among the others, then the sequence of this place
+            const int m = lane < p.batch ? sequence(p, lane).m : -1;
+            int place = 0;
+            for (int i = 0; i < 32; ++i) {
+                const int other = __shfl_sync(0xffffffffu, m, i);
+                place += other > m || (other == m && i < lane);
+            }
+            for (int i = 0; i < 32; ++i)
+                if (__shfl_sync(0xffffffffu, place, i) == lane) sequence_of = i;
+        }
+        all = 0;
+        for (int b0 = (p.batch - 1) / 32 * 32; b0 >= 0; b0 -= 32) {
+            count(p, b0, b0 ? b0 + lane : sequence_of);
+            all += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        const int ctas = gridDim.x, over = all % ctas;
+        apart = all - over;
+        until = !p.causal && over <= ctas / 2 ? all : apart;
+    }
+
+    __device__ __forceinline__ Item find(const AttentionArgs& p, int index) {
+        const int lane = threadIdx.x & 31;
+        int half = -1;  // both tiles
+        if (index >= apart) {
+            const int i = index - apart;
+            if (i < 2 * (until - apart)) {
+                index = apart + i / 2;
+                half = i & 1;
+            } else {
+                index -= until - apart;
+            }
+        }
+        Item it{};
+        if (index >= all) return it;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            if (p.batch > 32) count(p, b0, b0 ? b0 + lane : sequence_of);
+            const unsigned hit = __ballot_sync(0xffffffffu, incl > index);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                const int local = index - __shfl_sync(0xffffffffu, incl - mine, l);
+                const int blocks = __shfl_sync(0xffffffffu, mine, l) / p.Hk;
+                const Sequence s = sequence(p, b0 ? b0 + l : __shfl_sync(0xffffffffu, sequence_of, l));
+                it.any = 1;
+                it.q0 = s.q0;
+                it.n = s.n;
+                it.k0 = s.k0;
+                it.m = s.m;
+                it.hk = local % p.Hk;
+                it.token0 = (blocks - 1 - local / p.Hk) * 2 * tile_tokens + max(half, 0) * tile_tokens;
+                it.tiles = half < 0 && it.token0 + tile_tokens < s.n ? 2 : 1;
+                const int last = min(it.token0 + it.tiles * tile_tokens, s.n) - 1;
+                auto limit = [&](int token) { return p.causal ? clampi(token + s.m - s.n + 1, 0, s.m) : s.m; };
+                it.edge = limit(it.token0) / key_tile;
+                // (the second tile of an item taken apart may have no rows)
+                it.keys = it.token0 <= last ? (limit(last) + key_tile - 1) / key_tile : 0;
+                return it;
+            }
+            index -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+        return it;
+    }
+};
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -272,13 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&tmV);
             }
             const uint32_t q_bytes = L::kChunks * tile_tokens * p.group * 128;
+            Items items;
+            items.start(p, tile_tokens, kKeyTile);
             int index = blockIdx.x, edges = 0;
             int q_ph[2] = {1, 1};  // a fresh barrier lets the first wait through
             Ring<S> r;
             r.ph = 1;
             bool ok = true;
             for (int at = 0; ok; ++at) {
-                Item it = find_item(p, index, tile_tokens);
+                Item it = items.find(p, index);
                 if (!mbar_wait(&bars->item_empty[at & 1], ((at >> 1) & 1) ^ 1, 60)) {
                     it.any = 0;
                     ok = false;
@@ -493,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int lim, warp_lim;
             {
                 const int n = it.n, m = it.m, token = it.token0 + row_token;
-                const bool valid = used && token < n;
+                const bool valid = used && t < it.tiles && token < n;
                 lim = valid ? (p.causal ? clampi(token + m - n + 1, 0, m) : m) : 0;
                 warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : m);
             }
@@ -589,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int bad = tiles > 0 ? it.bad : 0;
             const int q0 = it.q0, k0 = it.k0, hk = it.hk, token = it.token0 + row_token, edge = it.edge;
-            const bool valid = used && token < it.n;
+            const bool valid = used && t < it.tiles && token < it.n;
             leave_item(at);
             const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
             const int head = hk * p.group + row_head;
@@ -698,7 +757,7 @@ cudaError_t launch_attention_prompt(const AttentionArgs& args, int dtype, int nu
         e = encode_heads(encode_fn, &map[2], 'V', a.v, dtype, a.Tk, a.Hk, a.D, a.v_token, a.v_head, 1, kKeyBox, detail,
                          n);
     if (e != cudaSuccess) return e;
-    const int64_t items = most_items(a);
+    const int64_t items = 2 * most_items(a);  // taken apart
     const int grid = items < num_sms ? static_cast<int>(items) : num_sms;
     if (dtype == kBf16)
         return a.D <= 64 ? launch_prompt_typed<__nv_bfloat16, 64>(map, a, grid, st)
