@@ -280,3 +280,70 @@ def test_python_refusals(w8a8):
     with pytest.raises(w8a8.W8A8Error, match="WORKSPACE"):
         w8a8.attention(q, k, v, workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
     assert w8a8.attention(q[:0], k, v).shape == (0, 4, 64)
+
+
+SCHEDULES = [
+    # (lens, Hq, Hk, D, causal): more items than SMs, leftovers taken apart, more than 32
+    # sequences, items of one tile between items of two, sequences without a row between
+    ([2048, 1000, 257, 77, 1, 1531], 32, 8, 128, True), ([640] * 5, 16, 8, 64, False), ([1024, 1024], 20, 20, 128, False),
+    ([1, 130, 0, 63, 257] * 9, 12, 4, 64, True), ([40] * 70, 8, 2, 128, True), ([3000], 16, 1, 64, False),
+    ([129, 128, 127] * 11 + [900], 4, 4, 128, True),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,causal", SCHEDULES)
+def test_many_items(w8a8, lens, hq, hk, d, causal):
+    q, k, v = make(lens, lens, hq, hk, d, FP16 if d == 64 else BF16, 71 + hq, fused=True)
+    cu = starts(lens)
+    for _ in range(2):  # the second call finds the counters as the first left them
+        o, lse = w8a8.attention(q, k, v, cu_q=cu, cu_k=cu, causal=causal, lse=True)
+        check(o, lse, q, k, v, lens, lens, causal, d ** -0.5)
+    assert w8a8.get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,m,queries_of", [(700, 700, "prompt"), (90, 2000, "prompt"), (1, 3000, "few"), (6, 1500, "few")])
+def test_scores_that_grow_with_the_key(w8a8, n, m, d, queries_of):
+    """Every key tile outweighs all before it (and, for half of the heads, every
+    tile is outweighed by the first): the softmax's reference moves each time."""
+    q, k, v = make([n], [m], 4, 2, d, BF16, 81 + d, fused=False)
+    ramp = torch.linspace(0, 40, m, device=DEV)[:, None]
+    k[:, 0, :1] += ramp.to(BF16)
+    k[:, 1, :1] -= ramp.to(BF16)
+    q[:, :, 0] = 8.0
+    cu_q, cu_k = starts([n]), starts([m])
+    for causal in (True, False):
+        o, lse = w8a8.attention(q, k, v, cu_q=cu_q, cu_k=cu_k, causal=causal, scale=1.0, lse=True)
+        check(o, lse, q, k, v, [n], [m], causal, 1.0)
+    assert w8a8.get_device_error() == (0, 0)
+
+
+def test_broadcast_keys_and_many_heads_a_group(w8a8):
+    """KV heads that are one head expanded, and more query heads on a KV head
+    than a tile of rows holds."""
+    q, k, v = make([150], [200], 6, 1, 64, BF16, 91, fused=False)
+    cu_q, cu_k = starts([150]), starts([200])
+    o, lse = w8a8.attention(q, k.expand(200, 3, 64), v.expand(200, 3, 64), cu_q=cu_q, cu_k=cu_k, lse=True)
+    check(o, lse, q, k, v, [150], [200], True, 0.125)
+    q, k, v = make([3], [900], 300, 2, 64, FP16, 92, fused=False)
+    o, lse = w8a8.attention(q, k, v, cu_q=starts([3]), cu_k=starts([900]), lse=True)
+    check(o, lse, q, k, v, [3], [900], True, 0.125)
+
+
+def test_calls_on_streams_of_their_own(w8a8):
+    """Overlapping calls on several streams, each with its stream's workspace."""
+    jobs = []
+    for i in range(4):
+        lens = torch.tensor([20000 + 777 * i, 100], dtype=torch.int32, device=DEV)
+        q = make([2], [1], 8, 2, 128, BF16, 101 + i, fused=False)[0]
+        kc, vc = make([1], [50000], 8, 2, 128, BF16, 105 + i, fused=False)[1:]
+        jobs.append((q, kc, vc, lens, w8a8.attention(q, kc, vc, k_lens=lens, batch=2)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        got = []
+        for s, (q, kc, vc, lens, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(w8a8.attention(q, kc, vc, k_lens=lens, batch=2))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, job[4]) for a, job in zip(got, jobs))
