@@ -529,7 +529,8 @@ def measure_imma_peak():
     return v.value
 
 
-from .operators import HALF, INTERLEAVED, attention, residual_norm_quant, rotary, rotary_append, \
-    rotary_frequencies  # noqa: E402
+from .operators import HALF, INTERLEAVED, attention, attention_workspace, residual_norm_quant, rotary, \
+    rotary_amplitude, rotary_append, rotary_frequencies  # noqa: E402
 from .module import Int8FFN, Int8Linear
+from .layer import Int8TransformerLayer  # noqa: E402
 from .pipeline import HostPipeline  # noqa: E402  (the modules use the functions above)
