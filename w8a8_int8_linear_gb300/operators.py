@@ -57,10 +57,12 @@ _attention_ws = {}
 
 
 def attention_workspace(device=None):
-    """A workspace for `attention`, for one stream at a time (its counters
-    start, and stay between calls, at zero)."""
+    """A workspace for `attention`, for one stream at a time (the counters at
+    its start are, and stay between calls, zero)."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    return torch.zeros(int(lib().w8a8_attention_workspace_size()), dtype=torch.uint8, device=device)
+    ws = torch.empty(lib().w8a8_attention_workspace_size(), dtype=torch.uint8, device=device)
+    ws[:lib().w8a8_attention_workspace_zeroed()].zero_()
+    return ws
 
 
 def _workspace_of(device, stream):
