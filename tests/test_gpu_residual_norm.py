@@ -173,3 +173,13 @@ def test_refusals(w8a8):
         with pytest.raises(err):
             call()
     assert f(x[:0], x[:0])[0].shape == (0, 64)
+
+
+@pytest.mark.parametrize("m,k,kind,dtype,branch,gamma,beta,groups,alpha", [
+    (2000, 4096, "layer", torch.float32, True, True, True, 7, 1.0), (1000, 5120, "rms", torch.float32, False, True, False, 1000, 1.0),
+    (1900, 8184, "layer", torch.float32, False, False, False, 3, -0.5), (913, 2056, "rms", torch.float32, True, False, True, None, 1.0),
+    (1300, 2048, "rms", BF16, False, True, False, 650, 1.0),
+])
+def test_groups_along_many_rows(w8a8, m, k, kind, dtype, branch, gamma, beta, groups, alpha):
+    """More rows than are worked on at once, so that each place for a row meets several groups."""
+    test_against_formula(w8a8, m, k, kind, dtype, branch, gamma, beta, groups, alpha)

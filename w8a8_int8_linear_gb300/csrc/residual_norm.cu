@@ -127,11 +127,38 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
         __syncthreads();
     }
 
+    // The options' values for this thread's columns stay in registers where they
+    // are few (a CTA's rows ascend, so it meets each group of rows once): fetched
+    // row by row they do not stay in L1 beside the ring, and the row waits for them.
+    constexpr bool kHold = kOptions && C == 1;
+    uint4 branch_w, gate_w, gamma_w, beta_w, scale_w, shift_w;
+    const auto hold = [&](const void* base, int64_t chunk, uint4& w) {
+        if (kHold && base && threadIdx.x < chunks) w = __ldg(static_cast<const uint4*>(base) + chunk + threadIdx.x);
+    };
+    hold(p.branch_gamma, 0, branch_w);
+    hold(p.gamma, 0, gamma_w);
+    hold(p.beta, 0, beta_w);
+    // modulation: the chunk where the present rows' starts, and the row where they end
+    int64_t mod = 0, mod_end = 0;
+    // chunk `chunk` of base, or what is held of it
+    auto option = [&](const void* base, int64_t chunk, const uint4& w, float(&v)[8]) {
+        if (kHold)
+            unpack8(w, v);
+        else
+            load8(base, chunk, v);
+    };
+
     int st = 0, phase = 0, odd = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, odd ^= 1) {
         const int64_t base = row * chunks;
-        const int64_t group = p.rows_per_group ? row / p.rows_per_group : 0;
-        const int64_t mod = group * (p.mod_stride >> 3);
+        if (kOptions && row >= mod_end) {
+            const int64_t group = p.rows_per_group ? row / p.rows_per_group : 0;
+            mod_end = p.rows_per_group ? (group + 1) * p.rows_per_group : p.M;
+            mod = group * (p.mod_stride >> 3);
+            hold(p.gate, mod, gate_w);
+            hold(p.mod_scale, mod, scale_w);
+            hold(p.mod_shift, mod, shift_w);
+        }
         if (kRing && !mbar_wait(&full[st], phase, 80)) {
             // recorded; the copies still on their way land before the CTA ends
             if (threadIdx.x == 0)
@@ -184,7 +211,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
         auto scaled = [&](int c, float(&v)[8]) {  // d -> v
             if (!p.gamma) return;
             float g[8];
-            load8(p.gamma, c, g);
+            option(p.gamma, c, gamma_w, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= g[j];
         };
@@ -196,12 +223,12 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
             unpack8(bw[i], h[i]);
             float g[8];
             if (p.branch_gamma) {
-                load8(p.branch_gamma, c, g);
+                option(p.branch_gamma, c, branch_w, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * branch * g[j];
             }
             if (p.gate) {
-                load8(p.gate, mod + c, g);
+                option(p.gate, mod + c, gate_w, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * g[j];
             }
@@ -276,17 +303,17 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
                 for (int j = 0; j < 8; ++j) h[i][j] *= r;
                 scaled(c, h[i]);
                 if (p.beta) {
-                    load8(p.beta, c, g);
+                    option(p.beta, c, beta_w, g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h[i][j] += g[j];
                 }
                 if (p.mod_scale) {
-                    load8(p.mod_scale, mod + c, g);
+                    option(p.mod_scale, mod + c, scale_w, g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j], g[j], h[i][j]);
                 }
                 if (p.mod_shift) {
-                    load8(p.mod_shift, mod + c, g);
+                    option(p.mod_shift, mod + c, shift_w, g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h[i][j] += g[j];
                 }
@@ -352,12 +379,12 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st)
     // store, more where a row passes several reductions.  Measured, CTAs x buffers:
     // 32768 x 5120 to the image 209 us at 2 x 3 (228 at 3 x 2, 235 at 4 x 2), 32768
     // x 4096 166 at 3 x 3 (189 at 4 x 2), x 8192 321 at 2 x 3 (356 at 3 x 2); with
-    // gate, scale and shift over fp32 16384 x 5120 198 at 3 x 2 (219 at 2 x 3),
-    // 4096 x 4096 46 at 4 x 2 (60 at 2 x 3).  So too where an SM has few rows to
+    // a branch norm 16384 x 5120 116 at 3 x 2 (132 at 2 x 3), 4096 x 4096 32 at 4 x 2
+    // (45 at 2 x 3).  So too where an SM has few rows to
     // share out: 4096 x 4096 to the image 22.8 at 4 x 2 (25.5 at 3 x 3).
     const bool many = kOptions || a.M < static_cast<int64_t>(num_sms) * 32;
     int per_sm = many ? 1024 / threads : (768 + threads / 2) / threads;
-    if (per_sm > 8) per_sm = 8;
+    if (per_sm > 16) per_sm = 16;
     if (per_sm < 1) per_sm = 1;
     int stages = many ? 2 : 3;
     while (per_sm > 1 && per_sm * stages * row_bytes > kRingBytes) --per_sm;
@@ -383,7 +410,18 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int num_sms, cudaStream_t st)
 
 template <bool kF32, bool kOptions>
 cudaError_t launch_width(const ResidualNormArgs& a, int num_sms, cudaStream_t st) {
-    return a.K <= 2048 ? launch_rows<1, kF32, kOptions>(a, num_sms, st) : launch_rows<2, kF32, kOptions>(a, num_sms, st);
+    // Narrow CTAs, so that more rows are on their way through their reductions: two
+    // chunks a thread from 512 elements on (16384 x 2048 with a branch norm 56 us
+    // against 72 with one, x 1024 32 against 38; x 512 21 with one against 23).  One
+    // chunk where the options are then held in registers and a CTA keeps them for
+    // several rows, if rows are long in bytes (fp32 x, gate, scale and shift: 4096 x
+    // 4096 37 us against 47 with two chunks, 4096 x 8192 71 against 87, 1000 x 4096
+    // 11.4 against 12.6; 600 x 4096 8.0 against 7.1).  In bf16 a row leaves less time
+    // than the fewer, wider CTAs take to reduce it (16384 x 5120 with a branch norm
+    // 172 against 116).
+    const bool wide = kF32 && kOptions && a.K <= 8192 && a.M >= static_cast<int64_t>(num_sms) * 6;
+    return wide || a.K <= 512 ? launch_rows<1, kF32, kOptions>(a, num_sms, st)
+                              : launch_rows<2, kF32, kOptions>(a, num_sms, st);
 }
 
 }  // namespace
