@@ -26,7 +26,8 @@
  *               Y = bf16_rne(acc + bias[n]) (add skipped when bias is NULL).
  *
  * Conventions for every entry point:
- *   - All matrices are row-major and dense (row stride = number of columns).
+ *   - All matrices are row-major and dense (row stride = number of columns),
+ *     but for the strides that the attention and rotary entry points take.
  *     X is [M,K] (tokens x input features), W is [N,K] (nn.Linear layout,
  *     Y = X * W^T), Y is [M,N].  bf16 arrays are passed as void pointers to
  *     IEEE bfloat16 values.
@@ -417,7 +418,7 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
  *   h  = alpha * X + gate * b'                      (gate absent: 1)
  *   n  = RMSNorm or LayerNorm (kind) of h, times gamma, plus beta
  *   y  = n * (1 + mod_scale) + mod_shift
- *   sx[m] = max|y[m,:]| / 127, code = clamp(rne(y * (1 / sx[m])), -127, 127)
+ *   sx[m] = max|y[m,:]| / 127, code = rne(y * (1 / sx[m])), at most 127 in size
  * in binary32 throughout: n is computed from the unrounded h and the codes
  * from the unrounded y.  The statistics are those of w8a8_norm_quant (both
  * norms use eps); the quantizer's conventions for an all-zero row are those

@@ -13,9 +13,15 @@
 // SM: warp 8 keeps the ring of key tiles full by TMA, also across items; warps
 // 0-3 and 4-7 take the tiles in turn, each warp its own 16 rows and its own part
 // of the tile's keys with an online softmax of its own (no barrier while keys
-// stream), and are joined at the end of an item.  An item that spans CTAs leaves (max, sum, unnormalized output)
-// per piece in the workspace; the CTA that arrives last joins the pieces in key
-// order, so the result does not depend on the order of arrival.
+// stream), and are joined at the end of an item.  An item that spans CTAs leaves
+// (max, sum, unnormalized output) per piece in the workspace; the CTA that
+// arrives last joins the pieces in key order, so the result does not depend on
+// the order of arrival.
+//
+// Measured with single queries, heads of 128, bf16: 131072 + 99991 keys of 8 KV
+// heads 141 us (0.99 of the copy bandwidth), 64 sequences of 1 to 4096 keys 92 us
+// (0.84: items start and end all along the way), 4 sequences of 77 to 513 keys
+// 11.7 us (start, one tile's latency, the join).
 //
 //   softmax:  t = scale log2(e) s;  running max M, sum L, O in binary32,
 //             p = 2^(t - M); P enters the second product rounded to the

@@ -1,5 +1,5 @@
 // What the attention kernels share: the sequences' bounds as the device holds
-// them, and warp-level tensor-core and copy building blocks.
+// them, and warp-level tensor-core building blocks.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -13,7 +13,6 @@
 namespace w8a8 {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -49,17 +48,6 @@ __device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
     }
     if (p.k_lens) s.m = clampi(p.k_lens[b], 0, s.m);
     return s;
-}
-
-// 16 bytes global -> shared, asynchronously; zeros where `take` is false.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-    const int bytes = take ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
