@@ -2,7 +2,8 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into one shared library with the CUDA runtime linked statically, so loading
-the library needs only the NVIDIA driver.  No fast-math: IEEE division and
+the library needs only the NVIDIA driver.  csrc/binding.cpp, which serves the
+Python calls of the operators, is linked to it and to torch.  No fast-math: IEEE division and
 square root, no flush-to-zero, and no contraction of separate multiplies and
 adds into fused multiply-adds (-fmad=false).
 """
@@ -11,12 +12,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libw8a8_gb300.so")
+BINDING = os.path.join(OUT_DIR, f"w8a8_binding_torch{torch.__version__}.so")  # of this torch's C++ interface
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm_s8.cu", "gemv.cu", "norm.cu", "imma_peak.cu",
            "attention.cu", "attention_prompt.cu", "rotary.cu", "residual_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,7 +44,7 @@ def _deps():
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -57,7 +62,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        obj = os.path.join(BUILD_DIR, "binding.o")
+        root = os.path.dirname(torch.__file__)
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+               "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
+               "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp]
@@ -65,6 +86,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", binding.result(), "-o", tmp, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + OUT_DIR, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
     return LIB
 
 
