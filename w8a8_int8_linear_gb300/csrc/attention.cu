@@ -58,7 +58,10 @@ struct SplitSmem {
     static constexpr int kStages = DP == 128 ? 4 : 8;
     static_assert(kStages % kGroups == 0, "one group per stage");
     static constexpr int kJoin = kStages * kStage;  // (max, sum, output) of four warps
-    static constexpr int kQ = kJoin + kWarps * 16 * (DP + 2) * 4;
+    // rows 8 floats further apart than they are long: the 8 rows that a warp writes at
+    // once fall into different banks
+    static constexpr int kJoinRow = DP + 8, kSlot = 16 * (2 + kJoinRow);
+    static constexpr int kQ = kJoin + kWarps * kSlot * 4;
     static constexpr int kBars = kQ + R * DP * 2;
     static constexpr int kTotal = kBars + 2 * kStages * 8;
 };
@@ -414,8 +417,8 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
         }
-        // a warp's [16] maxima, [16] sums, [16][DP] outputs
-        constexpr int kSlot = 16 * (DP + 2);
+        // a warp's [16] maxima, [16] sums, [16][kJoinRow] outputs
+        constexpr int kSlot = L::kSlot, kJoinRow = L::kJoinRow;
         float* slot = join + sub * kSlot;
         auto put = [&]() {
 #pragma unroll
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < kDT; ++j)
-                    *reinterpret_cast<float2*>(slot + 32 + r * DP + 8 * j + 2 * (lane & 3)) =
+                    *reinterpret_cast<float2*>(slot + 32 + r * kJoinRow + 8 * j + 2 * (lane & 3)) =
                         make_float2(o[j][2 * h], o[j][2 * h + 1]);
             }
         };
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
                 sum[h] = sum[h] * f0 + slot[16 + r] * f1;
 #pragma unroll
                 for (int j = 0; j < kDT; ++j) {
-                    const float2 v = *reinterpret_cast<const float2*>(slot + 32 + r * DP + 8 * j + 2 * (lane & 3));
+                    const float2 v = *reinterpret_cast<const float2*>(slot + 32 + r * kJoinRow + 8 * j + 2 * (lane & 3));
                     o[j][2 * h] = o[j][2 * h] * f0 + v.x * f1;
                     o[j][2 * h + 1] = o[j][2 * h + 1] * f0 + v.y * f1;
                 }
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
             float2 v[kPairs];
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
-                v[i] = *reinterpret_cast<const float2*>(pm + 32 + jr % 16 * DP + jc + 2 * kPer * i);
+                v[i] = *reinterpret_cast<const float2*>(pm + 32 + jr % 16 * kJoinRow + jc + 2 * kPer * i);
             join_into(pm[jr % 16], pm[16 + jr % 16], v);
         }
 
