@@ -57,11 +57,11 @@ struct SplitSmem {
     // even: a stage is always the same group's, whose waits then see every round of its barrier
     static constexpr int kStages = DP == 128 ? 4 : 8;
     static_assert(kStages % kGroups == 0, "one group per stage");
-    static constexpr int kJoin = kStages * kStage;  // (max, sum, output) of four warps
+    static constexpr int kJoin = kStages * kStage;  // (max, sum, output) of every warp
     // rows 8 floats further apart than they are long: the 8 rows that a warp writes at
     // once fall into different banks
     static constexpr int kJoinRow = DP + 8, kSlot = 16 * (2 + kJoinRow);
-    static constexpr int kQ = kJoin + kWarps * kSlot * 4;
+    static constexpr int kQ = kJoin + kGroups * kWarps * kSlot * 4;
     static constexpr int kBars = kQ + R * DP * 2;
     static constexpr int kTotal = kBars + 2 * kStages * 8;
 };
@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
             if (lane == 0) mbar_arrive(&empty[st]);
         }
 
-        // ---- join: group 1 into group 0 (the same warp and lane hold the same
-        // rows and columns), then the parts of the keys
+        // ---- join: every warp's rows to shared memory, then each thread its share of a
+        // row from the warps that have a part of it
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
@@ -419,42 +419,19 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
         }
         // a warp's [16] maxima, [16] sums, [16][kJoinRow] outputs
         constexpr int kSlot = L::kSlot, kJoinRow = L::kJoinRow;
-        float* slot = join + sub * kSlot;
-        auto put = [&]() {
+        float* slot = join + warp * kSlot;
+        // (the piece before has been read: its readers came through the barrier after Q)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 8 * h + (lane >> 2);
-                if ((lane & 3) == 0) {
-                    slot[r] = mx[h];
-                    slot[16 + r] = sum[h];
-                }
-#pragma unroll
-                for (int j = 0; j < kDT; ++j)
-                    *reinterpret_cast<float2*>(slot + 32 + r * kJoinRow + 8 * j + 2 * (lane & 3)) =
-                        make_float2(o[j][2 * h], o[j][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + (lane >> 2);
+            if ((lane & 3) == 0) {
+                slot[r] = mx[h];
+                slot[16 + r] = sum[h];
             }
-        };
-        named_bar_sync(1, kConsumers);  // the previous item's join is done
-        if (group == 1) put();
-        named_bar_sync(1, kConsumers);
-        if (group == 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 8 * h + (lane >> 2);
-                const float m1 = slot[r], nm = fmaxf(mx[h], m1);
-                const float f0 = mx[h] == nm ? 1.0f : exp2_approx(mx[h] - nm);
-                const float f1 = m1 == nm ? 1.0f : exp2_approx(m1 - nm);
-                mx[h] = nm;
-                sum[h] = sum[h] * f0 + slot[16 + r] * f1;
-#pragma unroll
-                for (int j = 0; j < kDT; ++j) {
-                    const float2 v = *reinterpret_cast<const float2*>(slot + 32 + r * kJoinRow + 8 * j + 2 * (lane & 3));
-                    o[j][2 * h] = o[j][2 * h] * f0 + v.x * f1;
-                    o[j][2 * h + 1] = o[j][2 * h + 1] * f0 + v.y * f1;
-                }
-            }
-            __syncwarp();  // the maxima and sums of a row are read by four lanes
-            put();
+            for (int j = 0; j < kDT; ++j)
+                *reinterpret_cast<float2*>(slot + 32 + r * kJoinRow + 8 * j + 2 * (lane & 3)) =
+                    make_float2(o[j][2 * h], o[j][2 * h + 1]);
         }
         named_bar_sync(1, kConsumers);
 
@@ -484,7 +461,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
         };
         clear();
 #pragma unroll
-        for (int x = 0; x < kParts; ++x) {
+        for (int x = 0; x < kGroups * kParts; ++x) {
             const float* pm = join + (x * kRowTiles + jr / 16) * kSlot;
             float2 v[kPairs];
 #pragma unroll
