@@ -435,72 +435,57 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
         }
         named_bar_sync(1, kConsumers);
 
-        // thread: row threadIdx.x / kPer, columns in pairs kPer apart
-        constexpr int kPer = kConsumers / R, kPairs = DP / 2 / kPer;
-        const int jr = threadIdx.x / kPer, jc = 2 * (threadIdx.x % kPer);
+        // A thread takes four columns of a row, of the rows that there are.
+        constexpr int kQuads = DP / 4, kPart = kPartFloats<DP, R>;
         const bool whole = t_begin == 0 && t_end == c.tiles;
-        float om = -INFINITY, ol = 0.0f;
-        float2 ov[kPairs];
-        auto clear = [&]() {
-            om = -INFINITY;
-            ol = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) ov[i] = make_float2(0.0f, 0.0f);
-        };
-        auto join_into = [&](float m, float l, const float2(&v)[kPairs]) {
-            const float nm = fmaxf(om, m);
-            const float f0 = om == nm ? 1.0f : exp2_approx(om - nm);
-            const float f1 = m == nm ? 1.0f : exp2_approx(m - nm);
-            ol = ol * f0 + l * f1;
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                ov[i].x = ov[i].x * f0 + v[i].x * f1;
-                ov[i].y = ov[i].y * f0 + v[i].y * f1;
+        float* part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (t_begin == 0 ? 1 : 0)) * kPart;
+        struct Row {
+            float m = -INFINITY, l = 0.0f;
+            float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            __device__ void add(float m1, float l1, const float4& v1, float f0, float f1) {
+                m = m1;
+                l = l * f0 + l1 * f1;
+                v = make_float4(v.x * f0 + v1.x * f1, v.y * f0 + v1.y * f1, v.z * f0 + v1.z * f1, v.w * f0 + v1.w * f1);
             }
-            om = nm;
         };
-        clear();
-#pragma unroll
-        for (int x = 0; x < kGroups * kParts; ++x) {
-            const float* pm = join + (x * kRowTiles + jr / 16) * kSlot;
-            float2 v[kPairs];
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                v[i] = *reinterpret_cast<const float2*>(pm + 32 + jr % 16 * kJoinRow + jc + 2 * kPer * i);
-            join_into(pm[jr % 16], pm[16 + jr % 16], v);
-        }
-
-        auto store = [&]() {
-            if (jr >= rows) return;
-            const int pr = rb * R + jr, i = pr / p.group, g = pr - i * p.group, head = hk * p.group + g;
+        auto weight = [](float m, float top) { return m == top ? 1.0f : exp2_approx(m - top); };
+        auto store = [&](const Row& row, int r, int col) {
+            const int pr = rb * R + r, i = pr / p.group, g = pr - i * p.group, head = hk * p.group + g;
             const bool sees = limit(pr) > 0;
-            const float inv = sees ? __frcp_rn(ol) : 0.0f;  // a row that sees keys of no weight is 0 / 0
-            T* dst = static_cast<T*>(p.o) + static_cast<int64_t>(s.q0 + i) * p.o_token +
-                     static_cast<int64_t>(head) * p.o_head;
-#pragma unroll
-            for (int x = 0; x < kPairs; ++x) {
-                const int cc = jc + 2 * kPer * x;
-                if (cc < p.D)
-                    *reinterpret_cast<uint32_t*>(dst + cc) =
-                        sees ? Pair16<T>::pack(ov[x].x * inv, ov[x].y * inv) : 0u;
-            }
-            if (p.lse && jc == 0)
-                p.lse[static_cast<int64_t>(s.q0 + i) * p.Hq + head] = sees ? (om + log2f(ol)) * kLn2 : -INFINITY;
+            const float inv = sees ? __frcp_rn(row.l) : 0.0f;  // a row that sees keys of no weight is 0 / 0
+            if (col < p.D)
+                *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + static_cast<int64_t>(s.q0 + i) * p.o_token +
+                                          static_cast<int64_t>(head) * p.o_head + col) =
+                    sees ? make_uint2(Pair16<T>::pack(row.v.x * inv, row.v.y * inv),
+                                      Pair16<T>::pack(row.v.z * inv, row.v.w * inv))
+                         : make_uint2(0, 0);
+            if (p.lse && col == 0)
+                p.lse[static_cast<int64_t>(s.q0 + i) * p.Hq + head] =
+                    sees ? (row.m + log2f(row.l)) * kLn2 : -INFINITY;
         };
-
-        if (whole) {
-            store();
-        } else {
-            // this piece's partial result, then the last piece to arrive joins all
-            constexpr int kPart = kPartFloats<DP, R>;
-            float* part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (t_begin == 0 ? 1 : 0)) * kPart;
-            if (jc == 0) {
-                part[jr] = om;
-                part[R + jr] = ol;
-            }
+#pragma unroll 1
+        for (int e = threadIdx.x; e < rows * kQuads; e += kConsumers) {
+            const int r = e / kQuads, col = 4 * (e % kQuads);
+            Row row;
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                *reinterpret_cast<float2*>(part + 2 * R + jr * DP + jc + 2 * kPer * i) = ov[i];
+            for (int x = 0; x < kGroups * kParts; ++x) {
+                const float* pm = join + (x * kRowTiles + r / 16) * kSlot;
+                const float m = pm[r % 16], top = fmaxf(row.m, m);
+                row.add(top, pm[16 + r % 16], *reinterpret_cast<const float4*>(pm + 32 + r % 16 * kJoinRow + col),
+                        weight(row.m, top), weight(m, top));
+            }
+            if (whole) {
+                store(row, r, col);
+            } else {
+                *reinterpret_cast<float4*>(part + 2 * R + r * DP + col) = row.v;
+                if (col == 0) {
+                    part[r] = row.m;
+                    part[R + r] = row.l;
+                }
+            }
+        }
+        if (!whole) {
+            // the last piece to arrive joins all, in the order of their keys
             __threadfence();
             named_bar_sync(1, kConsumers);
             const int first = static_cast<int>(quotient(item_start, per));
@@ -510,19 +495,41 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
             named_bar_sync(1, kConsumers);
             if (last_flag) {
                 __threadfence();
-                clear();
-#pragma unroll (R == 16 ? 4 : 1)
-                for (int x = first; x <= last; ++x) {
-                    // the first piece starts at the item's tile 0
-                    const float* src =
-                        p.partial + (2 * (static_cast<int64_t>(x) * p.side_heads + side) + (x == first)) * kPart;
-                    float2 v[kPairs];
+                constexpr int kBatch = 10;  // pieces on their way at once
+#pragma unroll 1
+                for (int e = threadIdx.x; e < rows * kQuads; e += kConsumers) {
+                    const int r = e / kQuads, col = 4 * (e % kQuads);
+                    Row row;
+#pragma unroll 1
+                    for (int x0 = first; x0 <= last; x0 += kBatch) {
+                        float m[kBatch], l[kBatch];
+                        float4 v[kBatch];
 #pragma unroll
-                    for (int i = 0; i < kPairs; ++i)
-                        v[i] = __ldcg(reinterpret_cast<const float2*>(src + 2 * R + jr * DP + jc + 2 * kPer * i));
-                    join_into(__ldcg(src + jr), __ldcg(src + R + jr), v);
+                        for (int i = 0; i < kBatch; ++i) {
+                            m[i] = -INFINITY;
+                            l[i] = 0.0f;
+                            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (x0 + i > last) continue;
+                            // the first piece starts at the item's tile 0
+                            const float* src =
+                                p.partial +
+                                (2 * (static_cast<int64_t>(x0 + i) * p.side_heads + side) + (x0 + i == first)) * kPart;
+                            m[i] = __ldcg(src + r);
+                            l[i] = __ldcg(src + R + r);
+                            v[i] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + r * DP + col));
+                        }
+                        float top = row.m;
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+                        float f = weight(row.m, top);
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            row.add(top, l[i], v[i], f, weight(m[i], top));
+                            f = 1.0f;
+                        }
+                    }
+                    store(row, r, col);
                 }
-                store();
                 if (threadIdx.x == 0) *counter = 0;  // ready for the next call
             }
         }
