@@ -347,3 +347,21 @@ def test_calls_on_streams_of_their_own(w8a8):
                 got.append(w8a8.attention(q, kc, vc, k_lens=lens, batch=2))
         torch.cuda.synchronize()
         assert all(torch.equal(a, job[4]) for a, job in zip(got, jobs))
+
+
+@pytest.mark.parametrize("hq,hk,d,dtype", [(32, 8, 128, BF16), (8, 2, 64, FP16), (6, 6, 72, BF16)])
+def test_caches_with_many_items(w8a8, hq, hk, d, dtype):
+    """More sequences than CTAs work on at once, of 0 to 700 keys; twice, as the
+    second call finds the counters as the first left them."""
+    lens = [(37 * i * i + 11 * i) % 701 for i in range(260)]
+    lens[5] = 0
+    cap = 704
+    q = make([1] * 260, [1], hq, hk, d, dtype, 111, fused=False)[0]
+    k, v = make([1], [260 * cap], hq, hk, d, dtype, 112, fused=False)[1:]
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for _ in range(2):
+        o, lse = w8a8.attention(q, k, v, k_lens=n, batch=260, lse=True)
+        for b in list(range(0, 260, 13)) + [5, 259]:
+            rows = slice(b * cap, b * cap + lens[b])
+            check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], k[rows], v[rows], [1], [lens[b]], True, d ** -0.5)
+    assert w8a8.get_device_error() == (0, 0)

@@ -10,18 +10,18 @@
 // keys, and cut into equal ranges whatever the lengths are; the lengths stay on
 // the device.  CTAs that run side by side take the same range for neighbouring
 // KV heads (up to 8), so that they read whole rows of the cache.  One CTA per
-// SM: warp 8 keeps the ring of key tiles full by TMA, also across items; warps
-// 0-3 and 4-7 take the tiles in turn, each warp its own 16 rows and its own part
-// of the tile's keys with an online softmax of its own (no barrier while keys
-// stream), and are joined at the end of an item.  An item that spans CTAs leaves
+// SM (or two of half the size): its last warp keeps the ring of key tiles full by
+// TMA, also across items; warps 0-3 and 4-7 take the tiles in turn, each warp its
+// own 16 rows and its own part of the tile's keys with an online softmax of its
+// own (no barrier while keys stream), and are joined at the end of an item.  An item that spans CTAs leaves
 // (max, sum, unnormalized output) per piece in the workspace; the CTA that
 // arrives last joins the pieces in key order, so the result does not depend on
 // the order of arrival.
 //
 // Measured with single queries, heads of 128, bf16: 131072 + 99991 keys of 8 KV
-// heads 141 us (0.99 of the copy bandwidth), 64 sequences of 1 to 4096 keys 92 us
-// (0.84: items start and end all along the way), 4 sequences of 77 to 513 keys
-// 11.7 us (start, one tile's latency, the join).
+// heads 139 us (the copy bandwidth), 64 sequences of 1 to 4096 keys 87 us (0.88: items
+// start and end all along the way), 4 sequences of 77 to 513 keys 9.3 us (launch,
+// one tile's latency, the join).
 //
 //   softmax:  t = scale log2(e) s;  running max M, sum L, O in binary32,
 //             p = 2^(t - M); P enters the second product rounded to the
@@ -41,27 +41,28 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int kGroups = 2;     // of consumer warps, which take tiles in turn
 constexpr int kWarps = 4;      // of a group
 constexpr int kKeys = 16;      // keys of a step
 constexpr int kTile = 64;
-constexpr int kConsumers = kGroups * kWarps * 32;
+constexpr int threads_of(int G) { return G * kWarps * 32 + 32; }
 
 // R: packed (query, head) rows of an item: 16, 32 or 64.  The four warps of a
 // group are R / 16 tiles of rows by 64 / R parts of the keys.
-template <int DP, int R>
+// G: groups of a CTA, which take its tiles in turn.  2: one CTA per SM; 1: two,
+// with half the ring each.
+template <int DP, int R, int G>
 struct SplitSmem {
     static constexpr int kChunk = kTile * 128;  // 64 elements of each key, 128-byte swizzled
     static constexpr int kKv = DP / 64 * kChunk;
     static constexpr int kStage = 2 * kKv;      // K, then V
     // even: a stage is always the same group's, whose waits then see every round of its barrier
-    static constexpr int kStages = DP == 128 ? 4 : 8;
-    static_assert(kStages % kGroups == 0, "one group per stage");
+    static constexpr int kStages = (DP == 128 ? 2 : 4) * G;
+    static_assert(kStages % G == 0, "one group per stage");
     static constexpr int kJoin = kStages * kStage;  // (max, sum, output) of every warp
     // rows 8 floats further apart than they are long: the 8 rows that a warp writes at
     // once fall into different banks
     static constexpr int kJoinRow = DP + 8, kSlot = 16 * (2 + kJoinRow);
-    static constexpr int kQ = kJoin + kGroups * kWarps * kSlot * 4;
+    static constexpr int kQ = kJoin + G * kWarps * kSlot * 4;
     static constexpr int kBars = kQ + R * DP * 2;
     static constexpr int kTotal = kBars + 2 * kStages * 8;
 };
@@ -120,14 +121,14 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
-template <typename T, int DP, int R>
-__global__ void __launch_bounds__(kConsumers + 32, 1)
+template <typename T, int DP, int R, int G>
+__global__ void __launch_bounds__(threads_of(G), 3 - G)
     attention_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const AttentionArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int last_flag;
-    using L = SplitSmem<DP, R>;
-    constexpr int S = L::kStages;
+    using L = SplitSmem<DP, R, G>;
+    constexpr int S = L::kStages, kConsumers = threads_of(G) - 32;
     constexpr int kRowTiles = R / 16, kParts = kWarps / kRowTiles;
     constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
     constexpr int kDT = DP / 8;       // 8-wide output column tiles
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
         }
     };
 
-    if (warp == kGroups * kWarps) {
+    if (warp == G * kWarps) {
         // ---- producer
         bool ok = true;
         int loaded = 0;
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
 
 #pragma unroll 1
         for (int t = t_begin; t < end; ++t, turn ^= 1, next_stage()) {
-            if (turn != group) continue;
+            if (G > 1 && turn != group) continue;
             ok = ok && mbar_wait(&full[st], ph, 52);
             const uint32_t ks = smem_u32(smem) + st * L::kStage, vs = ks + L::kKv;
 #pragma unroll 1
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
             const int r = e / kQuads, col = 4 * (e % kQuads);
             Row row;
 #pragma unroll
-            for (int x = 0; x < kGroups * kParts; ++x) {
+            for (int x = 0; x < G * kParts; ++x) {
                 const float* pm = join + (x * kRowTiles + r / 16) * kSlot;
                 const float m = pm[r % 16], top = fmaxf(row.m, m);
                 row.add(top, pm[16 + r % 16], *reinterpret_cast<const float4*>(pm + 32 + r % 16 * kJoinRow + col),
@@ -537,29 +538,40 @@ __global__ void __launch_bounds__(kConsumers + 32, 1)
     }
 }
 
-template <typename T, int DP, int R>
-cudaError_t launch_split_rows(const CUtensorMap (&map)[2], const AttentionArgs& a, int ctas, cudaStream_t st) {
+template <typename T, int DP, int R, int G>
+cudaError_t launch_split_rows(const CUtensorMap (&map)[2], const AttentionArgs& a, int num_sms, cudaStream_t st) {
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SplitSmem<DP, R>::kTotal);
+        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SplitSmem<DP, R, G>::kTotal);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
-    attention_split_kernel<T, DP, R><<<ctas, kConsumers + 32, SplitSmem<DP, R>::kTotal, st>>>(map[0], map[1], a);
+    const int ctas = (3 - G) * num_sms / a.side_heads * a.side_heads;
+    attention_split_kernel<T, DP, R, G><<<ctas, threads_of(G), SplitSmem<DP, R, G>::kTotal, st>>>(map[0], map[1], a);
     return cudaGetLastError();
 }
 
 template <typename T, int DP>
-cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, int num_sms, cudaStream_t st) {
     // as many rows an item as a sequence has, so that its keys are read once
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.group;
-    if (rows <= 16 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 16>(map, a, ctas, st);
-    if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32>(map, a, ctas, st);
-    return launch_split_rows<T, DP, 64>(map, a, ctas, st);
+    if (rows <= 16 * static_cast<int64_t>(a.batch)) {
+        // Two CTAs per SM where they get several items each: one starts and ends an
+        // item while the other's keys stream (us, against one CTA, at heads of 128, 8
+        // KV heads: 64 sequences of 60 keys 10.6 against 16.4, 256 of 500 96 against
+        // 104, 64 of 1 to 4096 87 against 89).  Not where items are cut over the CTAs,
+        // into twice as many pieces (16 of 8192 86 against 84, on 1 KV head 27 against
+        // 24, 4 of 500 9.8 against 9.5).
+        const int64_t items = static_cast<int64_t>(a.batch) * (a.Hk / a.side_heads);
+        if (2 * items >= 3 * (num_sms / a.side_heads)) return launch_split_rows<T, DP, 16, 1>(map, a, num_sms, st);
+        return launch_split_rows<T, DP, 16, 2>(map, a, num_sms, st);
+    }
+    if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32, 2>(map, a, num_sms, st);
+    return launch_split_rows<T, DP, 64, 2>(map, a, num_sms, st);
 }
 
 // Heads that run side by side: the largest divisor of Hk up to 8.
@@ -571,8 +583,10 @@ int side_heads(int Hk) {
 
 }  // namespace
 
-size_t attention_counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 4 + 255) / 256 * 256; }
+// a counter for each of up to two CTAs per SM
+size_t attention_counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 8 + 255) / 256 * 256; }
 
+// two pieces a CTA, of 64 rows, or of 16 where two CTAs run per SM
 size_t attention_workspace_bytes(int num_sms) {
     return attention_counter_bytes(num_sms) + static_cast<size_t>(num_sms) * 2 * kPartFloats<128, 64> * 4;
 }
@@ -626,11 +640,10 @@ cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num
                              detail, n);
         if (e != cudaSuccess) return e;
     }
-    const int ctas = num_sms / a.side_heads * a.side_heads;
     if (dtype == kBf16)
-        return a.D <= 64 ? launch_split<__nv_bfloat16, 64>(map, a, ctas, st)
-                         : launch_split<__nv_bfloat16, 128>(map, a, ctas, st);
-    return a.D <= 64 ? launch_split<__half, 64>(map, a, ctas, st) : launch_split<__half, 128>(map, a, ctas, st);
+        return a.D <= 64 ? launch_split<__nv_bfloat16, 64>(map, a, num_sms, st)
+                         : launch_split<__nv_bfloat16, 128>(map, a, num_sms, st);
+    return a.D <= 64 ? launch_split<__half, 64>(map, a, num_sms, st) : launch_split<__half, 128>(map, a, num_sms, st);
 }
 
 cudaError_t attention_split_read_device_error(unsigned int* code) {
