@@ -511,19 +511,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                          mbar_wait(&bars->kv_full[lv % S], (lv / S) & 1, 73);
                     if (!ok) break;
                     const uint32_t v = pipe + (lv % S) * L::kTileBytes;
-#pragma unroll 8
-                    for (int c = me; c < L::kTileBytes / 16; c += 64) {
-                        uint4 w;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(v + 16 * c));
-                        if (any_non_finite<T>(w)) {
-                            constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-                            uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    constexpr int kAtOnce = 8;  // loads in flight: one by one they would bound an item's end
+                    static_assert(L::kTileBytes % (16 * 64 * kAtOnce) == 0, "whole rounds");
+                    for (int c0 = me; c0 < L::kTileBytes / 16; c0 += 64 * kAtOnce) {
+                        uint4 w[kAtOnce];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if ((u[i] & e) == e) u[i] &= 0xFFFF0000u;
-                                if (((u[i] >> 16) & e) == e) u[i] &= 0x0000FFFFu;
+                        for (int i = 0; i < kAtOnce; ++i)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                                         : "r"(v + 16 * (c0 + 64 * i)));
+                        bool some = false;
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i) some |= any_non_finite<T>(w[i]);
+                        if (!some) continue;
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            if (!any_non_finite<T>(w[i])) continue;
+                            const int c = c0 + 64 * i;
+                            constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+                            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((u[k] & e) == e) u[k] &= 0xFFFF0000u;
+                                if (((u[k] >> 16) & e) == e) u[k] &= 0x0000FFFFu;
                             }
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v + 16 * c), "r"(u[0]),
                                          "r"(u[1]), "r"(u[2]), "r"(u[3])
