@@ -661,19 +661,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l0, l1;
             f2_unpack(sum2, l0, l1);
             const float l = l0 + l1;
+            const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
+            // where the rows go: through shared memory, so that eight lanes write 128
+            // bytes of a row, this lane 16 bytes of rows sub, sub + 4, ...
+            const int q0 = it.q0, k0 = it.k0, hk = it.hk, token = it.token0 + row_token, edge = it.edge;
+            const bool valid = used && t < it.tiles && token < it.n;
+            const int head = hk * p.group + row_head;
+            const int sub = lane >> 3, ch = lane & 7;
+            const int64_t mine = static_cast<int64_t>(q0 + token) * p.o_token + static_cast<int64_t>(head) * p.o_head;
+            const uint32_t valid_rows = __ballot_sync(0xffffffffu, valid) >> sub;
+            int64_t to_row[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) to_row[x] = __shfl_sync(0xffffffffu, mine, 4 * x + sub) + 8 * ch;
             if (tiles > 0) ok = ok && mbar_wait(&bars->pv_done[t][(own - 1) & 3], ((own - 1) >> 2) & 1, 76);
             if (!ok) break;
             tc_fence_after();
             const int bad = tiles > 0 ? it.bad : 0;
-            const int q0 = it.q0, k0 = it.k0, hk = it.hk, token = it.token0 + row_token, edge = it.edge;
-            const bool valid = used && t < it.tiles && token < it.n;
             leave_item(at);
-            const float inv = lim > 0 ? __frcp_rn(l) : 0.0f;
-            const int head = hk * p.group + row_head;
-            const int64_t mine = static_cast<int64_t>(q0 + token) * p.o_token + static_cast<int64_t>(head) * p.o_head;
-            // through shared memory, so that eight lanes write 128 bytes of a row
             const uint32_t stage = smem_u32(smem) + L::kOut + warp * L::kOutBytes;
-            const int sub = lane >> 3, ch = lane & 7;
 #pragma unroll 1
             for (int i = 0; i < DP / 64; ++i) {
 #pragma unroll
@@ -710,17 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
+                uint4 w[8];
 #pragma unroll
-                for (int r0 = 0; r0 < 32; r0 += 4) {
-                    const int r = r0 + sub;
-                    const int64_t at_r = __shfl_sync(0xffffffffu, mine, r);
-                    const bool take = __shfl_sync(0xffffffffu, valid, r) && 64 * i + 8 * ch < p.D;
-                    uint4 w;
+                for (int x = 0; x < 8; ++x)
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                 : "r"(stage + r * 128 + ((ch ^ (r & 7)) << 4))
-                                 : "memory");
-                    if (take) *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + at_r + 64 * i + 8 * ch) = w;
+                                 : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
+                                 : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
+                if (64 * i + 8 * ch < p.D) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (valid_rows >> (4 * x) & 1) *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + to_row[x] + 64 * i) = w[x];
                 }
                 __syncwarp();
             }
