@@ -35,13 +35,14 @@
 // the output.  The two halves of P go to the second product one after the
 // other.
 //
-// Bound by the tensor cores: for D = 128 two tiles alternate at 0.97 of their
-// rate while key tiles stream; what an item costs besides (its first product,
-// the last softmax and O on the way out), the causal tiles' unseen half and the
-// last wave take the rest.  Measured: 8192 tokens causal, 40 heads on 8 of 128,
-// 450 us, 1530 TFLOP/s; 16384 x 8 heads full 655 us, 1690 TFLOP/s.  For D = 64 a
-// key tile's products take half as long and its softmax does not: 4096 x 32 heads
-// full 130 us, 1050 TFLOP/s.
+// Bound by the tensor cores: for D = 128 two tiles alternate at 0.95 of their
+// rate while key tiles stream (2900 clocks a pair of tiles).  An item costs about
+// 4000 clocks besides (the last softmax, the last product, O on its way out, 64 KB
+// at the 64 bytes a clock that an SM stores), and so do the causal tiles' unseen
+// half and the last wave.  Measured: 8192 tokens causal, 40 heads on 8 of 128, 434
+// us, 1580 TFLOP/s; 16384 x 8 heads full 650 us, 1690 TFLOP/s.  For D = 64 a key
+// tile's products take half as long and its softmax does not: 4096 x 32 heads full
+// 129 us, 1060 TFLOP/s.
 //
 // A weight of 0 does not hide a non-finite V (0 * inf = NaN).  In the key tiles
 // that some row does not see completely, warps 10-11 therefore replace the
