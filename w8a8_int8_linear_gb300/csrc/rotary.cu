@@ -43,22 +43,25 @@ __device__ __forceinline__ float half_turns(int64_t p, double f) {
 }
 
 // Rotate 8 pairs: the half layout holds the x of pairs 0..7 in a and the y in
-// b; the interleaved one x0 y0 x1 y1 ... across a then b.
+// b; the interleaved one x0 y0 x1 y1 ... across a then b.  cs: (cos, sin) of
+// pairs 0 and 1, `step` further on of 2 and 3, and so on.
 template <typename T, bool kHalf>
-__device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float2* cs) {
+__device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float4* cs, int step) {
     uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+    auto turn = [](uint32_t& w, float c, float s) {  // x y of one pair
+        const float2 x = Pair16<T>::unpack(w);
+        w = Pair16<T>::pack(fmaf(x.x, c, -(x.y * s)), fmaf(x.y, c, x.x * s));
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const float4 t = cs[i * step];
         if (kHalf) {
             const float2 x = Pair16<T>::unpack(u[i]), y = Pair16<T>::unpack(v[i]);
-            const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
-            u[i] = Pair16<T>::pack(fmaf(x.x, t0.x, -(y.x * t0.y)), fmaf(x.y, t1.x, -(y.y * t1.y)));
-            v[i] = Pair16<T>::pack(fmaf(y.x, t0.x, x.x * t0.y), fmaf(y.y, t1.x, x.y * t1.y));
+            u[i] = Pair16<T>::pack(fmaf(x.x, t.x, -(y.x * t.y)), fmaf(x.y, t.z, -(y.y * t.w)));
+            v[i] = Pair16<T>::pack(fmaf(y.x, t.x, x.x * t.y), fmaf(y.y, t.z, x.y * t.w));
         } else {
-            const float2 x = Pair16<T>::unpack(u[i]), y = Pair16<T>::unpack(v[i]);
-            const float2 t0 = cs[i], t1 = cs[4 + i];
-            u[i] = Pair16<T>::pack(fmaf(x.x, t0.x, -(x.y * t0.y)), fmaf(x.y, t0.x, x.x * t0.y));
-            v[i] = Pair16<T>::pack(fmaf(y.x, t1.x, -(y.y * t1.y)), fmaf(y.y, t1.x, y.x * t1.y));
+            turn(i < 2 ? u[2 * i] : v[2 * i - 4], t.x, t.y);
+            turn(i < 2 ? u[2 * i + 1] : v[2 * i - 3], t.z, t.w);
         }
     }
     a = make_uint4(u[0], u[1], u[2], u[3]);
@@ -70,11 +73,14 @@ constexpr int kAtOnce = 3;  // units of a thread in flight
 // One CTA per token.  The angles of its pairs are computed once, in shared
 // memory, while the first units of Q and K (8 pairs of a head each) are on
 // their way to registers; bytes bound it: 32768 tokens x (40 + 8) heads x 128
-// in 126 us are 0.94 of the copy bandwidth (133 us with 4 units, and with the
-// loads after the angles).
+// take 117 us, the copy bandwidth (126 with the angles in order, where the units
+// of eight neighbouring threads share two banks; 4 units in flight, or the loads
+// after the angles, were 5% slower).
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p) {
-    __shared__ float2 cs[kMaxPairs];
+    // two pairs each: those of a unit lie a head's units apart, so that the units of
+    // neighbouring threads fall into different banks
+    __shared__ float4 cs[kMaxPairs / 2];
     const int64_t t = blockIdx.x;
     const int pairs = p.rot >> 1;
     // the cache row of this token's K and V; outside the cache: not stored
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
     for (int u0 = threadIdx.x; !angles || u0 < units; u0 += kAtOnce * kRotThreads) {
         uint4 a[kAtOnce], b[kAtOnce];
         T* dst[kAtOnce];
-        int pair[kAtOnce];
+        int unit[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             const int u = u0 + i * kRotThreads;
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
             const bool is_q = u < q_units;
             const int v = is_q ? u : u - q_units, h = v / per_head, k = v - h * per_head;
             const T* src = is_q ? q_src + h * p.q.head : k_src + h * p.k.head;
-            pair[i] = 8 * k;
+            unit[i] = k;
             const int at = kHalf ? 8 * k : 16 * k;
             dst[i] = (is_q ? q_dst + h * p.q_out.head : k_dst + h * p.k_out.head) + at;
             a[i] = *reinterpret_cast<const uint4*>(src + at);
@@ -115,7 +121,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
             for (int i = threadIdx.x; i < pairs; i += kRotThreads) {
                 float s, c;
                 sincospif(half_turns(pos, p.freqs[i]), &s, &c);
-                cs[i] = make_float2(c * p.amplitude, p.inverse ? -(s * p.amplitude) : s * p.amplitude);
+                reinterpret_cast<float2*>(cs)[2 * ((i >> 1 & 3) * per_head + (i >> 3)) + (i & 1)] =
+                    make_float2(c * p.amplitude, p.inverse ? -(s * p.amplitude) : s * p.amplitude);
             }
             __syncthreads();
             angles = true;
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             if (!dst[i]) continue;
-            rotate8<T, kHalf>(a[i], b[i], cs + pair[i]);
+            rotate8<T, kHalf>(a[i], b[i], cs + unit[i], per_head);
             *reinterpret_cast<uint4*>(dst[i]) = a[i];
             *reinterpret_cast<uint4*>(dst[i] + (kHalf ? pairs : 8)) = b[i];
         }
