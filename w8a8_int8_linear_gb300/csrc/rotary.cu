@@ -138,9 +138,22 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
 
     // 16-byte chunks that are only copied: past the rotated part, and V
     auto copy = [&](const T* src, T* dst, int heads, int64_t from, int64_t to, int first, int chunks) {
-        for (int u = threadIdx.x; u < heads * chunks; u += kRotThreads) {
-            const int h = u / chunks, i = first + 8 * (u - h * chunks);
-            *reinterpret_cast<uint4*>(dst + h * to + i) = *reinterpret_cast<const uint4*>(src + h * from + i);
+        const int all = heads * chunks;
+        for (int u0 = threadIdx.x; u0 < all; u0 += kAtOnce * kRotThreads) {
+            uint4 w[kAtOnce];
+            T* at[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int u = u0 + i * kRotThreads;
+                at[i] = nullptr;
+                if (u >= all) continue;
+                const int h = u / chunks, c = first + 8 * (u - h * chunks);
+                w[i] = *reinterpret_cast<const uint4*>(src + h * from + c);
+                at[i] = dst + h * to + c;
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (at[i]) *reinterpret_cast<uint4*>(at[i]) = w[i];
         }
     };
     const int rest = (p.dim - p.rot) >> 3;
