@@ -389,9 +389,9 @@ typedef enum {
  * angle is reduced exactly for any 64-bit position; cos and sin are binary32.
  *   Q [T,Hq,D], K [T,Hk,D] (NULL with Hk = 0), Q_out, K_out: dtype BF16 or
  *   FP16, last dimension dense, token and head strides in elements
- *   (multiples of 8).  An output may be its input (same pointer and strides);
- *   otherwise they must not overlap.  D % 8 == 0, D <= 256, rot % 16 == 0,
- *   0 < rot <= D.
+ *   (multiples of 8, an output's not 0).  An output may be its input (same
+ *   pointer and strides); otherwise they must not overlap.  D % 8 == 0,
+ *   D <= 256, rot % 16 == 0, 0 < rot <= D.
  *   positions [T] int64, freqs [rot/2] fp64 (radians per position), device.
  * w8a8_rotary_append also copies V and writes K and V to rows slots[t] (int64,
  * device) of K_cache / V_cache [cache_rows,Hk,D]; a slot outside

@@ -105,3 +105,11 @@ def test_workspace_sizes_need_a_device(L):
         assert size > zeroed > 0 and size % 256 == 0 and zeroed % 256 == 0
     else:
         assert L.w8a8_attention_workspace_size() == 0 and L.w8a8_attention_workspace_zeroed() == 0
+
+
+def test_rotary_outputs_on_one_another(L):
+    for f, n in ((rotary, 8), (append, 12)):
+        for i in range(n // 2, n):
+            s = [256, 64] + [128, 64] * (n // 2 - 1)
+            s[i] = 0
+            assert f(L, strides=s) == INVALID, (f, i)

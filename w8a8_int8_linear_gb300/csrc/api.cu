@@ -696,6 +696,10 @@ w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_
         if (!h->ptr) return W8A8_ERR_INVALID_ARG;
         if (h->token < 0 || h->head < 0 || h->token % 8 != 0 || h->head % 8 != 0 || !aligned16(h->ptr))
             return W8A8_ERR_ALIGNMENT;
+        // rows of an output that lie on one another
+        if ((h == &a.q_out || h == &a.k_out || h == &a.v_out) && a.tokens > 1 &&
+            (h->token == 0 || (h->head == 0 && h->heads > 1)))
+            return W8A8_ERR_INVALID_ARG;
     }
     if ((reinterpret_cast<uintptr_t>(a.positions) & 7u) || (reinterpret_cast<uintptr_t>(a.slots) & 7u) ||
         (reinterpret_cast<uintptr_t>(a.freqs) & 7u))
@@ -703,7 +707,7 @@ w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_
     DeviceInfo dev;
     w8a8_status s = current_device(&dev);
     if (s != W8A8_OK) return s;
-    return from_cuda(w8a8::launch_rotary(a, dtype, layout == W8A8_ROTARY_HALF, st), "rotary launch");
+    return from_cuda(w8a8::launch_rotary(a, dtype, layout == W8A8_ROTARY_HALF, dev.num_sms, st), "rotary launch");
 }
 
 }  // namespace

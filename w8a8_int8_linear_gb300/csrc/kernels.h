@@ -148,7 +148,7 @@ struct RotaryArgs {
     int dim, rot, inverse;
     float amplitude;
 };
-cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, cudaStream_t st);
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, int num_sms, cudaStream_t st);
 
 // Branch norm, gate, residual, norm, modulation and quantization of [M, K]
 // rows; every pointer after B but H may be nullptr.

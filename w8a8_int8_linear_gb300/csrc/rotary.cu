@@ -26,7 +26,6 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int kRotThreads = 128;
 constexpr int kMaxPairs = 128;  // heads of at most 256 elements
 
 // The angle p f in half turns, in [-1, 1).
@@ -76,7 +75,7 @@ constexpr int kAtOnce = 3;  // units of a thread in flight
 // take 117 us, the copy bandwidth (126 with the angles in order, where the units
 // of eight neighbouring threads share two banks; 4 units in flight, or the loads
 // after the angles, were 5% slower).
-template <typename T, bool kHalf>
+template <typename T, bool kHalf, int kRotThreads>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p) {
     // two pairs each: those of a unit lie a head's units apart, so that the units of
     // neighbouring threads fall into different banks
@@ -165,17 +164,29 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
              p.dim >> 3);
 }
 
-}  // namespace
-
-cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, cudaStream_t st) {
+template <int kRotThreads>
+void launch_threads(const RotaryArgs& a, int dtype, bool half, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>(a.tokens));
     if (dtype == kBf16) {
-        if (half) rotary_kernel<__nv_bfloat16, true><<<grid, kRotThreads, 0, st>>>(a);
-        else rotary_kernel<__nv_bfloat16, false><<<grid, kRotThreads, 0, st>>>(a);
+        if (half) rotary_kernel<__nv_bfloat16, true, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
+        else rotary_kernel<__nv_bfloat16, false, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
     } else {
-        if (half) rotary_kernel<__half, true><<<grid, kRotThreads, 0, st>>>(a);
-        else rotary_kernel<__half, false><<<grid, kRotThreads, 0, st>>>(a);
+        if (half) rotary_kernel<__half, true, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
+        else rotary_kernel<__half, false, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
     }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, int num_sms, cudaStream_t st) {
+    // 64 threads where a token has no more units than they keep in flight, so that
+    // more tokens are on their way (8192 tokens x 48 heads of 64 15.9 us against 18.8
+    // with 128, half of heads of 128 33.1 against 36.2; whole heads of 128 32.9 against
+    // 32.1), and where eight CTAs of 128 per SM would not hold all tokens (1500 tokens
+    // 4.8 against 5.4, 1000 4.1 against 4.0)
+    const int units = (a.q.heads + a.k.heads) * (a.rot >> 4);
+    if (units <= 64 * kAtOnce && a.tokens > static_cast<int64_t>(num_sms) * 8) launch_threads<64>(a, dtype, half, st);
+    else launch_threads<128>(a, dtype, half, st);
     return cudaGetLastError();
 }
 
