@@ -365,3 +365,22 @@ def test_caches_with_many_items(w8a8, hq, hk, d, dtype):
             rows = slice(b * cap, b * cap + lens[b])
             check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], k[rows], v[rows], [1], [lens[b]], True, d ** -0.5)
     assert w8a8.get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("lens,queries,hq,hk,d", [
+    ([300] * 8, 1, 32, 8, 128), ([420, 367, 0, 172], 1, 32, 8, 64), ([4871], 4, 12, 1, 128), ([64, 65, 1, 640, 0, 129], 2, 28, 4, 72),
+    ([3471, 2395, 2544, 2414], 1, 12, 1, 64), ([500] * 31 + [7000], 1, 16, 2, 128), ([130] * 32, 3, 8, 8, 128), ([90000, 3, 70], 1, 8, 8, 128),
+])
+def test_caches_cut_into_pieces(w8a8, lens, queries, hq, hk, d):
+    """Few tiles of keys for many CTAs: whole ranges an item, and the joins; twice,
+    as the second call finds the counters as the first left them."""
+    n, cap = len(lens), max(lens) + 5
+    q = make([queries] * n, [1], hq, hk, d, BF16, 121, fused=False)[0]
+    k, v = make([1], [n * cap], hq, hk, d, BF16, 122, fused=False)[1:]
+    on_gpu = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for _ in range(2):
+        o, lse = w8a8.attention(q, k, v, k_lens=on_gpu, batch=n, lse=True)
+        for b in range(n):
+            rows, mine = slice(b * cap, b * cap + lens[b]), slice(b * queries, (b + 1) * queries)
+            check(o[mine], lse[mine], q[mine], k[rows], v[rows], [queries], [lens[b]], True, d ** -0.5)
+    assert w8a8.get_device_error() == (0, 0)

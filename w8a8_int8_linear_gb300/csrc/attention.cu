@@ -98,14 +98,16 @@ __device__ __forceinline__ int blocks_of(const AttentionArgs& p, const Sequence&
 }
 __device__ __forceinline__ int tiles_of(const Sequence& s) { return max(1, (s.m + kTile - 1) / kTile); }
 
-// Tiles of the 32 sequences from b0 on: this lane's, and inclusive over the lanes.
+// Tiles of the 32 sequences from b0 on: this lane's, and inclusive over the
+// lanes; `most` becomes the most of one item.
 template <int R>
-__device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64_t& mine, int64_t& incl) {
+__device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64_t& mine, int64_t& incl, int& most) {
     const int lane = threadIdx.x & 31;
     mine = 0;
     if (b0 + lane < p.batch) {
         const Sequence s = sequence(p, b0 + lane);
         mine = static_cast<int64_t>(blocks_of<R>(p, s)) * (p.Hk / p.side_heads) * tiles_of(s);
+        most = max(most, tiles_of(s));
     }
     incl = mine;
 #pragma unroll
@@ -113,6 +115,12 @@ __device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64
         const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
     }
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // a / b for positive a and b, in 32 bits where a allows.
@@ -153,23 +161,66 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     // sequences' counts stay
     const int side = blockIdx.x % p.side_heads, range = blockIdx.x / p.side_heads, ranges = gridDim.x / p.side_heads;
     const int head_groups = p.Hk / p.side_heads;
-    int64_t mine, incl;
-    tiles_from<R>(p, 0, mine, incl);
-    int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    for (int b0 = 32; b0 < p.batch; b0 += 32) {
-        int64_t m2, i2;
-        tiles_from<R>(p, b0, m2, i2);
-        total += __shfl_sync(0xffffffffu, i2, 31);
+    Sequence own = {0, 0, 0, 0};  // this lane's, of up to 32
+    if (p.batch <= 32 && lane < p.batch) own = sequence(p, lane);
+    const int blocks = blocks_of<R>(p, own), items = blocks * head_groups, tiles = tiles_of(own);
+    int64_t mine = static_cast<int64_t>(items) * tiles, incl, total;
+    int most = tiles;
+    const bool few = p.batch <= 32 && !__any_sync(0xffffffffu, mine > 1 << 24);  // fits 32 bits
+    if (few) {
+        total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine));
+    } else {
+        tiles_from<R>(p, 0, mine, incl, most);
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        for (int b0 = 32; b0 < p.batch; b0 += 32) {
+            int64_t m2, i2;
+            tiles_from<R>(p, b0, m2, i2, most);
+            total += __shfl_sync(0xffffffffu, i2, 31);
+        }
     }
-    const int64_t per = max(int64_t(1), quotient(total + ranges - 1, ranges));
+    // A piece takes a CTA 0.35 us a tile (of 16 rows; 64 rows four times that), and the
+    // join 0.08 us a piece for each of its rounds over the rows: few tiles are not cut
+    // into more pieces than that is worth (12 heads on 1, one sequence of 4871 keys 14
+    // us against 24).
+    const int least = max(1, static_cast<int>(sqrt_approx(0.23f * 16 / R * p.join_rounds * __reduce_max_sync(0xffffffffu, most))));
+    int64_t per = max(static_cast<int64_t>(least), quotient(total + ranges - 1, ranges));
+    // A CTA whose range ends one item and begins another takes 3 us longer: where
+    // there are few tiles, ranges of a few more that start with the items are better
+    // (8 sequences of 300 keys 10.8 us against 13.3).  An item then takes whole ranges
+    // of the line of tiles.
+    int line = tiles;  // an item's part of the line
+    bool apart = false;
+    if (few) {
+        if (total <= 64 * ranges) {
+            for (int wide = static_cast<int>(per), end = wide + 4; wide <= end; ++wide) {
+                const int pieces = (tiles + wide - 1) / wide;
+                if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(items * pieces)) > static_cast<unsigned>(ranges))
+                    continue;
+                apart = true;
+                per = wide;
+                line = pieces * wide;
+                break;
+            }
+        }
+        const int n = items * line;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += t;
+        }
+        mine = n;
+        incl = sum;
+        total = __shfl_sync(0xffffffffu, sum, 31);
+    }
     int64_t w = per * range;
-    const int64_t w_end = min(total, w + per);
+    int64_t w_end = min(total, w + per);
     if (w >= w_end) return;
     Cursor c;
     {  // the cursor of tile w
         int64_t left = w;
         for (int b0 = 0;; b0 += 32) {
-            if (b0 > 0) tiles_from<R>(p, b0, mine, incl);
+            if (b0 > 0) tiles_from<R>(p, b0, mine, incl, most);
             const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
             if (hit) {
                 const int l = __ffs(hit) - 1;
@@ -179,11 +230,20 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
             }
             left -= __shfl_sync(0xffffffffu, incl, 31);
         }
-        c.s = sequence(p, c.b);
-        c.blocks = blocks_of<R>(p, c.s);
-        c.tiles = tiles_of(c.s);
-        c.item = static_cast<int>(quotient(left, c.tiles));
-        c.tile = static_cast<int>(left - static_cast<int64_t>(c.item) * c.tiles);
+        if (few) {
+            const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, c.b); };
+            c.s = {of(own.q0), of(own.n), of(own.k0), of(own.m)};
+            c.blocks = of(blocks);
+            c.tiles = of(tiles);
+            line = of(line);
+        } else {
+            c.s = sequence(p, c.b);
+            c.blocks = blocks_of<R>(p, c.s);
+            line = c.tiles = tiles_of(c.s);
+        }
+        c.item = static_cast<int>(quotient(left, line));
+        c.tile = static_cast<int>(left - static_cast<int64_t>(c.item) * line);
+        if (apart) w_end = w + min(per, static_cast<int64_t>(c.tiles - c.tile));
     }
     __syncthreads();
 
@@ -631,6 +691,9 @@ cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num
     a.counters = static_cast<int*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attention_counter_bytes(num_sms));
     a.side_heads = side_heads(a.Hk);
+    // rows of an item x 32 (16) quads of columns, over the 256 threads of a CTA
+    const int64_t rows = (static_cast<int64_t>(a.Tq) * a.group + a.batch - 1) / a.batch;
+    a.join_rounds = static_cast<int>(((rows < 64 ? rows : 64) * (a.D <= 64 ? 16 : 32) + 255) / 256);
     CUtensorMap map[2] = {};  // without keys, nothing is loaded
     if (a.Tk > 0) {
         cudaError_t e = encode_heads(encode_fn, &map[0], 'K', a.k, dtype, a.Tk, a.Hk, a.D, a.k_token, a.k_head, 1,

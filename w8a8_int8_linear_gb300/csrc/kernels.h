@@ -111,6 +111,7 @@ struct AttentionArgs {
     // filled in by the launchers
     int* counters;
     float* partial;
+    int join_rounds;         // of the split kernel's threads over the rows of an item
     int side_heads;
 };
 size_t attention_workspace_bytes(int num_sms);
