@@ -19,8 +19,8 @@
 // the order of arrival.
 //
 // Measured with single queries, heads of 128, bf16: 131072 + 99991 keys of 8 KV
-// heads 139 us (the copy bandwidth), 64 sequences of 1 to 4096 keys 87 us (0.88: items
-// start and end all along the way), 4 sequences of 77 to 513 keys 9.5 us (launch,
+// heads 139 us (the copy bandwidth), 64 sequences of 1 to 4096 keys 88 us (0.88: items
+// start and end all along the way), 4 sequences of 77 to 513 keys 9.8 us (launch,
 // one tile's latency, the join).
 //
 //   softmax:  t = scale log2(e) s;  running max M, sum L, O in binary32,
