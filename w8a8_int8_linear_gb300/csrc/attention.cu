@@ -13,10 +13,10 @@
 // SM (or two of half the size): its last warp keeps the ring of key tiles full by
 // TMA, also across items; warps 0-3 and 4-7 take the tiles in turn, each warp its
 // own 16 rows and its own part of the tile's keys with an online softmax of its
-// own (no barrier while keys stream), and are joined at the end of an item.  An item that spans CTAs leaves
-// (max, sum, unnormalized output) per piece in the workspace; the CTA that
-// arrives last joins the pieces in key order, so the result does not depend on
-// the order of arrival.
+// own (no barrier while keys stream), and are joined at the end of an item.  An
+// item that spans CTAs leaves (max, sum, unnormalized output) per piece in the
+// workspace; the CTA that arrives last joins the pieces in key order, so the
+// result does not depend on the order of arrival.
 //
 // Measured with single queries, heads of 128, bf16: 131072 + 99991 keys of 8 KV
 // heads 139 us (the copy bandwidth), 64 sequences of 1 to 4096 keys 88 us (0.88: items
