@@ -656,9 +656,9 @@ size_t attention_workspace_bytes(int num_sms) {
 // above, by what a key costs.  The prompt kernel takes 7 ns a key for each wave
 // of items (a pair of 128-row tiles per SM), the split kernel 0.13 ns for each
 // block of 64 rows, and 2 us more around them.  Measured at 40 query heads on 8
-// KV heads x 128: 1 sequence x 64 queries over 32768 keys 198 us split against
-// 356, 4 x 8 over 32768 165 against 242, 4 x 16 289 against 242, 16 x 8 over
-// 4096 98 against 54, 1 x 4 over 512 15.2 against 13.6.
+// KV heads x 128: 1 sequence x 64 queries over 32768 keys 202 us split against
+// 357, 4 x 8 over 32768 163 against 236, 4 x 16 293 against 236, 16 x 8 over
+// 4096 98 against 49, 1 x 4 over 512 13.7 against 11.3.
 bool attention_splits(const AttentionArgs& a, int num_sms) {
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.group, batch = a.batch;
     if (rows <= 16 * batch) return true;
