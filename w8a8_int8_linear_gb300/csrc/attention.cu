@@ -652,7 +652,8 @@ size_t attention_workspace_bytes(int num_sms) {
 }
 
 // Whether to split the keys over the CTAs rather than run the prompt kernel:
-// always up to one MMA tile of rows per sequence (the keys' bytes bound it);
+// always up to one MMA tile of rows per sequence (the keys' bytes bound it) and
+// where there are no keys, which the split kernel runs without loading any;
 // above, by what a key costs.  The prompt kernel takes 7 ns a key for each wave
 // of items (a pair of 128-row tiles per SM), the split kernel 0.13 ns for each
 // block of 64 rows, and 2 us more around them.  Measured at 40 query heads on 8
@@ -661,7 +662,7 @@ size_t attention_workspace_bytes(int num_sms) {
 // 4096 98 against 49, 1 x 4 over 512 13.7 against 11.3.
 bool attention_splits(const AttentionArgs& a, int num_sms) {
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.group, batch = a.batch;
-    if (rows <= 16 * batch) return true;
+    if (rows <= 16 * batch || a.Tk == 0) return true;  // (there is no tensor map of no keys)
     if (a.group > 128 || a.Tk < 1024 * batch) return a.group > 128;
     const int64_t blocks = (rows + 64 * batch - 1) / (64 * batch) * batch * a.Hk;
     const int64_t tokens = 2 * (128 / a.group);  // of an item of the prompt kernel
