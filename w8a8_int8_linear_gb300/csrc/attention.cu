@@ -26,7 +26,10 @@
 //   softmax:  t = scale log2(e) s;  running max M, sum L, O in binary32,
 //             p = 2^(t - M); P enters the second product rounded to the
 //             inputs' type (half a step, 2^-8 for bf16, of each p: the same
-//             size as the output's own rounding, the sums stay binary32).
+//             size as the output's own rounding, the sums stay binary32), in
+//             fp16 times 2^15, so that only weights below 2^-29 lose bits of it
+//             (2^-40 of a row's largest at most; 8 multiplications a step of 16
+//             keys, exact ones).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     constexpr int kRowTiles = R / 16, kParts = kWarps / kRowTiles;
     constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
     constexpr int kDT = DP / 8;       // 8-wide output column tiles
+    constexpr float kScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;  // of p and O, not of the sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* empty = full + S;
@@ -427,8 +431,10 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
                     apart = __any_sync(0xffffffffu, bad);
                 }
                 if (!apart) {
-                    const uint32_t pf[4] = {Pair16<T>::pack(sc[0][0], sc[0][1]), Pair16<T>::pack(sc[0][2], sc[0][3]),
-                                            Pair16<T>::pack(sc[1][0], sc[1][1]), Pair16<T>::pack(sc[1][2], sc[1][3])};
+                    uint32_t pf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pf[i] = Pair16<T>::pack(sc[i >> 1][2 * (i & 1)] * kScale, sc[i >> 1][2 * (i & 1) + 1] * kScale);
 #pragma unroll
                     for (int j = 0; j < kDT; j += 2) {
                         uint32_t vf[4];
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
                             const float odd = k & 8 ? sc[1][e + 1] : sc[0][e + 1];
                             return __shfl_sync(0xffffffffu, k & 1 ? odd : even, from);
                         };
-                        const float p0 = pick(0), p1 = pick(2);
+                        const float p0 = pick(0) * kScale, p1 = pick(2) * kScale;
                         const bool s0 = key0 + k < lim[0], s1 = key0 + k < lim[1];
 #pragma unroll
                         for (int j = 0; j < kDT; ++j) {
@@ -513,7 +519,8 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
         auto store = [&](const Row& row, int r, int col) {
             const int pr = rb * R + r, i = pr / p.group, g = pr - i * p.group, head = hk * p.group + g;
             const bool sees = limit(pr) > 0;
-            const float inv = sees ? __frcp_rn(row.l) : 0.0f;  // a row that sees keys of no weight is 0 / 0
+            // (a row that sees keys of no weight is 0 / 0)
+            const float inv = sees ? __frcp_rn(row.l) * (1.0f / kScale) : 0.0f;
             if (col < p.D)
                 *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + static_cast<int64_t>(s.q0 + i) * p.o_token +
                                           static_cast<int64_t>(head) * p.o_head + col) =

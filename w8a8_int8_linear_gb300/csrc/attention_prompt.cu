@@ -32,8 +32,9 @@
 // it.  It moves only when a score exceeds it by more than 2^8 in weight; only
 // then is O_t rescaled (by the softmax threads, between products).  Sums and O
 // stay binary32; P's rounding to 16 bits is half a step of each weight, as in
-// the output.  The two halves of P go to the second product one after the
-// other.
+// the output.  In fp16 M lies 7 lower, so that weights reach 2^15 and only those
+// below 2^-14 (2^-21 of the row's largest at most) lose bits, of 2^-25 (2^-32 of
+// it).  The two halves of P go to the second product one after the other.
 //
 // Bound by the tensor cores: for D = 128 two tiles alternate at 0.95 of their
 // rate while key tiles stream (2900 clocks a pair of tiles).  An item costs about
@@ -66,6 +67,8 @@ constexpr int kKeyTile = 128;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr float kSlack = 8.0f;  // log2 of the weight that moves the reference
+template <typename T>
+constexpr float kShift = std::is_same<T, __half>::value ? 7.0f : 0.0f;  // log2 of the weight at the reference
 constexpr int kChunkBytes = 128 * 128;  // 128 rows of 64 16-bit elements
 
 template <int DP>
@@ -577,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int both = it.tiles, tiles = t < both ? it.keys : 0;
             float ref = -INFINITY;
+            auto base_of = [](float r) { return r == -INFINITY ? 0.0f : kShift<T> - r; };
             uint64_t sum2 = f2_pack(0.0f, 0.0f);
             for (int j = 0; j < tiles; ++j, ++own) {
                 const int buf = (steps + j * both + t) % L::kBuffers;
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     const bool moves = top > ref + kSlack;  // also from -inf
                     if (__any_sync(0xffffffffu, moves)) {
-                        const float f = moves ? exp2_approx(ref - top) : 1.0f;
+                        const float f = moves ? exp2_approx((kShift<T> - top) - (kShift<T> - ref)) : 1.0f;
                         if (moves) ref = top;
                         sum2 = f2_mul(sum2, f2_pack(f, f));
                         // S of this step says nothing of the product before it
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const float base = ref == -INFINITY ? 0.0f : -ref;
+                const float base = base_of(ref);
                 const uint64_t base2 = f2_pack(base, base);
                 uint64_t part2[2] = {sum2, f2_pack(0.0f, 0.0f)};
 #pragma unroll
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.lse && valid)
                 p.lse[static_cast<int64_t>(q0 + token) * p.Hq + head] =
-                    lim > 0 ? ((ref == -INFINITY ? 0.0f : ref) + log2f(l)) * kLn2 : -INFINITY;
+                    lim > 0 ? (log2f(l) - base_of(ref)) * kLn2 : -INFINITY;
             tc_fence_before();
         }
     }
