@@ -422,7 +422,9 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
  * in binary32 throughout: n is computed from the unrounded h and the codes
  * from the unrounded y.  The statistics are those of w8a8_norm_quant (both
  * norms use eps); the quantizer's conventions for an all-zero row are those
- * of w8a8_quantize_act.
+ * of w8a8_quantize_act.  A row with a y that is not finite gets an sx that is
+ * not finite (its codes then mean nothing), so that no finite numbers follow
+ * from it; other rows are not touched by it.
  *   X, H [M,K] residual stream in / out, x_dtype BF16 or FP32 (H may be X);
  *   B [M,K] bf16 the branch; branch_gamma, gamma, beta [K] bf16 or NULL;
  *   gate, mod_scale, mod_shift bf16 or NULL: row m uses row m / rows_per_group,

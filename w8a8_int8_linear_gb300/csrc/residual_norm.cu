@@ -47,9 +47,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// Maxima that a NaN stays in: a row that has one somewhere gets the scale NaN, and
+// the Linear after it gives NaN rather than its bias.
 __device__ __forceinline__ float warp_max_abs(float v) {
     float m;
-    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+__device__ __forceinline__ float max_abs(float top, float v) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(top), "f"(fabsf(v)));
     return m;
 }
 
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
                 if (!kOptions) {
                     scaled(c, h[i]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                    for (int j = 0; j < 8; ++j) top = max_abs(top, h[i][j]);
                 }
             }
         }
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
                 if (!kOptions) {
                     scaled(c, h[i]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                    for (int j = 0; j < 8; ++j) top = max_abs(top, h[i][j]);
                 }
             }
             all = block_reduce<true, !kOptions>(s, top, red[odd][2]);
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const ResidualNo
                 }
                 if (p.sx) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[i][j]));
+                    for (int j = 0; j < 8; ++j) top = max_abs(top, h[i][j]);
                 }
             }
             if (p.sx) peak = block_reduce<false, true>(0.0f, top, red[odd][3]).y;
