@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/w8a8.h"
+#include "device_errors.h"
 #include "gemv.h"
 #include "kernels.h"
 
@@ -828,18 +829,11 @@ w8a8_status w8a8_get_device_error(int* code) {
         cudaGetLastError();
         return W8A8_ERR_CUDA;
     }
-    unsigned int v = 0, vs = 0, vq = 0;
-    if (w8a8::gemm_read_device_error(&v) != cudaSuccess) return W8A8_ERR_CUDA;
-    if (w8a8::gemm_s8_read_device_error(&vs) != cudaSuccess) return W8A8_ERR_CUDA;
-    if (w8a8::quant_read_device_error(&vq) != cudaSuccess) return W8A8_ERR_CUDA;
-    unsigned int va = 0, vr = 0;
-    if (w8a8::attention_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
-    if (va == 0 && w8a8::attention_split_read_device_error(&va) != cudaSuccess) return W8A8_ERR_CUDA;
-    if (w8a8::residual_norm_read_device_error(&vr) != cudaSuccess) return W8A8_ERR_CUDA;
-    if (v == 0) v = vs;
-    if (v == 0) v = vq;
-    if (v == 0) v = va;
-    if (v == 0) v = vr;
+    cudaError_t (*const readers[])(unsigned int*) = {
+        w8a8::gemm_read_device_error,      w8a8::gemm_s8_read_device_error,         w8a8::quant_read_device_error,
+        w8a8::attention_read_device_error, w8a8::attention_split_read_device_error, w8a8::residual_norm_read_device_error};
+    unsigned int v = 0;
+    if (w8a8::read_device_errors(readers, &v) != cudaSuccess) return W8A8_ERR_CUDA;
     *code = static_cast<int>(v);
     if (v >= w8a8::kDeviceErrorTimeoutBase) return W8A8_ERR_TIMEOUT;
     return v ? W8A8_ERR_CUDA : W8A8_OK;
