@@ -698,8 +698,8 @@ w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_
         if (h->token < 0 || h->head < 0 || h->token % 8 != 0 || h->head % 8 != 0 || !aligned16(h->ptr))
             return W8A8_ERR_ALIGNMENT;
         // rows of an output that lie on one another
-        if ((h == &a.q_out || h == &a.k_out || h == &a.v_out) && a.tokens > 1 &&
-            (h->token == 0 || (h->head == 0 && h->heads > 1)))
+        if ((h == &a.q_out || h == &a.k_out || h == &a.v_out) &&
+            ((h->token == 0 && a.tokens > 1) || (h->head == 0 && h->heads > 1)))
             return W8A8_ERR_INVALID_ARG;
     }
     if ((reinterpret_cast<uintptr_t>(a.positions) & 7u) || (reinterpret_cast<uintptr_t>(a.slots) & 7u) ||
