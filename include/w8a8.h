@@ -361,7 +361,7 @@ typedef enum { W8A8_BF16 = 0, W8A8_FP16 = 1, W8A8_FP32 = 2 } w8a8_dtype;
  *   k_lens[b] rows of the part are keys (a cache that is not full).  Values
  *   outside the tensors' rows are clamped to them.  Rows of O that belong to
  *   no sequence are not written.
- *   scale > 0, finite.
+ *   scale > 0, and scale * log2(e) within binary32 (up to 2.35e38).
  *   workspace: w8a8_attention_workspace_size() bytes, 256-byte aligned.  Its
  *   first w8a8_attention_workspace_zeroed() bytes must be zero before its
  *   first use; every call leaves them zero.  Calls that may overlap on the

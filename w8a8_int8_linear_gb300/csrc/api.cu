@@ -619,7 +619,8 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
                            void* stream) {
     if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
     if (batch < 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return W8A8_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
+    const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;  // the kernels' exponentials are 2^x
+    if (!(scale > 0.0f) || !(scale_log2 <= 3.4e38)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
     if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || Tk > INT32_MAX ||
         batch > INT32_MAX || Tq * (Hq / Hk) > INT32_MAX)
         return W8A8_ERR_SHAPE;
@@ -662,7 +663,7 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
     a.v_head = v_head;
     a.o_token = o_token;
     a.o_head = o_head;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.scale_log2 = static_cast<float>(scale_log2);
     a.causal = causal != 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* enc = encode_fn();
