@@ -67,6 +67,31 @@ bool truth(PyObject* o) {
     return v != 0;
 }
 
+// An argument that may be a tensor, by its place.
+struct Argument {
+    int at;
+    const char* name;
+};
+
+// The kernels run on the GPU of the first tensor; the others must be on it too
+// (what is no CUDA tensor at all is refused by name later on).
+template <size_t N>
+void one_device(PyObject* const* a, const Argument (&arguments)[N]) {
+    const Argument* first = nullptr;
+    c10::Device device(c10::kCUDA);
+    for (const Argument& g : arguments) {
+        if (!THPVariable_Check(a[g.at])) continue;
+        const Tensor& t = THPVariable_Unpack(a[g.at]);
+        if (!t.is_cuda()) continue;
+        if (!first) {
+            first = &g;
+            device = t.device();
+        } else if (t.device() != device) {
+            value_error(std::string(g.name) + " is on " + t.device().str() + ", " + first->name + " on " + device.str());
+        }
+    }
+}
+
 w8a8_dtype dtype_of(ScalarType t) {
     return t == ScalarType::BFloat16 ? W8A8_BF16 : t == ScalarType::Half ? W8A8_FP16 : W8A8_FP32;
 }
@@ -144,6 +169,7 @@ Tensor workspace_of(const Tensor& like, cudaStream_t stream) {
 
 // Q, K, V, cu_q, cu_k, k_lens, batch, causal, scale, out, lse, workspace
 PyObject* attention(PyObject* const* a) {
+    one_device(a, {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "cu_q"}, {4, "cu_k"}, {5, "k_lens"}, {9, "out"}, {11, "workspace"}});
     Tensor q = tensor(a[0], "Q"), k = tensor(a[1], "K"), v = tensor(a[2], "V");
     Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -197,6 +223,7 @@ Turns turns(PyObject* positions, PyObject* freqs, int64_t tokens) {
 
 // Q, K, positions, freqs, layout, amplitude, inverse, q_out, k_out
 PyObject* rotary(PyObject* const* a) {
+    one_device(a, {{0, "Q"}, {1, "K"}, {2, "positions"}, {3, "freqs"}, {7, "q_out"}, {8, "k_out"}});
     const Tensor& q = tensor(a[0], "Q");
     const Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -220,6 +247,8 @@ PyObject* rotary(PyObject* const* a) {
 
 // Q, K, V, positions, freqs, k_cache, v_cache, slots, layout, amplitude, q_out
 PyObject* rotary_append(PyObject* const* a) {
+    one_device(a, {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "positions"}, {4, "freqs"}, {5, "k_cache"}, {6, "v_cache"},
+                   {7, "slots"}, {10, "q_out"}});
     const Tensor& q = tensor(a[0], "Q");
     const Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -258,6 +287,8 @@ void* dense(PyObject* o, const char* name, ScalarType type, at::IntArrayRef shap
 // X, B, gamma, beta, eps, kind, alpha, gate, branch_gamma, mod_scale, mod_shift,
 // rows_per_group, h_out, image, codes, y
 PyObject* residual_norm_quant(PyObject* const* a) {
+    one_device(a, {{0, "X"}, {1, "B"}, {2, "gamma"}, {3, "beta"}, {7, "gate"}, {8, "branch_gamma"}, {9, "mod_scale"},
+                   {10, "mod_shift"}, {12, "h_out"}});
     if (!THPVariable_Check(a[0]) || THPVariable_Unpack(a[0]).dim() != 2) value_error("X must be a [rows, width] tensor");
     const Tensor& x = THPVariable_Unpack(a[0]);
     const ScalarType type = x.scalar_type(), bf16 = ScalarType::BFloat16;
