@@ -1,4 +1,5 @@
-"""Refusals of tensors on several GPUs by the operators' Python calls.  The
+"""Refusals of tensors on several GPUs, and of written tensors that require a
+gradient, by the operators' Python calls.  The
 tensors are fake ones, which have a device and no memory: nothing is launched.
 Where there is a GPU, torch makes none of another that is not there."""
 import pytest
@@ -44,4 +45,16 @@ def test_another_gpu(w, call, name):
     first = next(iter(CALLS[call]))
     args = {n: on("cuda:1" if n == name else "cuda:0", *spec) for n, spec in CALLS[call].items()}
     with pytest.raises(ValueError, match=f"{name} is on cuda:1, {first} on cuda:0"):
+        getattr(w, call)(**args)
+
+
+WRITTEN = {"attention": ["out"], "rotary": ["q_out", "k_out"], "rotary_append": ["k_cache", "v_cache", "q_out"],
+           "residual_norm_quant": ["h_out"]}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in WRITTEN.items() for n in names])
+def test_written_tensors_that_require_a_gradient(w, call, name):
+    args = {n: on("cuda:0", *spec) for n, spec in CALLS[call].items()}
+    args[name].requires_grad_()
+    with pytest.raises(ValueError, match=f"{name} requires a gradient"):
         getattr(w, call)(**args)

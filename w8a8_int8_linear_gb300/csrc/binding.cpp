@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -71,17 +72,22 @@ bool truth(PyObject* o) {
 struct Argument {
     int at;
     const char* name;
+    bool written = false;  // by the call, where it is given
 };
 
 // The kernels run on the GPU of the first tensor; the others must be on it too
-// (what is no CUDA tensor at all is refused by name later on).
+// (what is no CUDA tensor at all is refused by name later on).  What is written
+// in place has no gradient: autograd would give that of the value before.
 template <size_t N>
-void one_device(PyObject* const* a, const Argument (&arguments)[N]) {
+void check_arguments(PyObject* const* a, const Argument (&arguments)[N]) {
     const Argument* first = nullptr;
     c10::Device device(c10::kCUDA);
     for (const Argument& g : arguments) {
         if (!THPVariable_Check(a[g.at])) continue;
         const Tensor& t = THPVariable_Unpack(a[g.at]);
+        if (g.written && t.requires_grad() && c10::GradMode::is_enabled())
+            value_error(std::string(g.name) + " requires a gradient and cannot be written in place: detach it, or call "
+                        "under torch.no_grad()");
         if (!t.is_cuda()) continue;
         if (!first) {
             first = &g;
@@ -89,6 +95,17 @@ void one_device(PyObject* const* a, const Argument (&arguments)[N]) {
         } else if (t.device() != device) {
             value_error(std::string(g.name) + " is on " + t.device().str() + ", " + first->name + " on " + device.str());
         }
+    }
+}
+
+// Autograd learns that they were written, so that a backward pass which needs a
+// value from before says so (tensors made in inference mode have no version).
+template <size_t N>
+void bump_written(PyObject* const* a, const Argument (&arguments)[N]) {
+    for (const Argument& g : arguments) {
+        if (!g.written || none(a[g.at])) continue;
+        const Tensor& t = THPVariable_Unpack(a[g.at]);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     }
 }
 
@@ -169,7 +186,9 @@ Tensor workspace_of(const Tensor& like, cudaStream_t stream) {
 
 // Q, K, V, cu_q, cu_k, k_lens, batch, causal, scale, out, lse, workspace
 PyObject* attention(PyObject* const* a) {
-    one_device(a, {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "cu_q"}, {4, "cu_k"}, {5, "k_lens"}, {9, "out"}, {11, "workspace"}});
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "cu_q"}, {4, "cu_k"}, {5, "k_lens"},
+                                             {9, "out", true}, {11, "workspace"}};
+    check_arguments(a, arguments);
     Tensor q = tensor(a[0], "Q"), k = tensor(a[1], "K"), v = tensor(a[2], "V");
     Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -203,6 +222,7 @@ PyObject* attention(PyObject* const* a) {
         dtype_of(type), batch, hq.tokens, hk.tokens, hq.heads, hk.heads, hq.dim, hq.token, hq.head, hk.token, hk.head,
         hv.token, hv.head, ho.token, ho.head, static_cast<float>(scale), truth(a[7]), ws.data_ptr(), ws.nbytes(), stream);
     if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
     if (!lse.defined()) return wrap(out);
     return Py_BuildValue("(NN)", wrap(out), wrap(lse));
 }
@@ -223,7 +243,9 @@ Turns turns(PyObject* positions, PyObject* freqs, int64_t tokens) {
 
 // Q, K, positions, freqs, layout, amplitude, inverse, q_out, k_out
 PyObject* rotary(PyObject* const* a) {
-    one_device(a, {{0, "Q"}, {1, "K"}, {2, "positions"}, {3, "freqs"}, {7, "q_out"}, {8, "k_out"}});
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "K"}, {2, "positions"}, {3, "freqs"}, {7, "q_out", true},
+                                             {8, "k_out", true}};
+    check_arguments(a, arguments);
     const Tensor& q = tensor(a[0], "Q");
     const Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -242,13 +264,16 @@ PyObject* rotary(PyObject* const* a) {
         hk.token, hk.head, qo.token, qo.head, ko.token, ko.head, tu.positions, tu.freqs, static_cast<float>(number(a[5])),
         static_cast<w8a8_rotary_layout>(integer(a[4])), truth(a[6]), c10::cuda::getCurrentCUDAStream().stream());
     if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
     return Py_BuildValue("(NN)", wrap(q_out), wrap(k_out));
 }
 
 // Q, K, V, positions, freqs, k_cache, v_cache, slots, layout, amplitude, q_out
 PyObject* rotary_append(PyObject* const* a) {
-    one_device(a, {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "positions"}, {4, "freqs"}, {5, "k_cache"}, {6, "v_cache"},
-                   {7, "slots"}, {10, "q_out"}});
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "positions"}, {4, "freqs"},
+                                             {5, "k_cache", true}, {6, "v_cache", true}, {7, "slots"},
+                                             {10, "q_out", true}};
+    check_arguments(a, arguments);
     const Tensor& q = tensor(a[0], "Q");
     const Heads hq = heads(q, "Q");
     const ScalarType type = q.scalar_type();
@@ -270,6 +295,7 @@ PyObject* rotary_append(PyObject* const* a) {
         cv.head, tu.positions, slots, tu.freqs, static_cast<float>(number(a[9])),
         static_cast<w8a8_rotary_layout>(integer(a[8])), c10::cuda::getCurrentCUDAStream().stream());
     if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
     return wrap(q_out);
 }
 
@@ -287,8 +313,10 @@ void* dense(PyObject* o, const char* name, ScalarType type, at::IntArrayRef shap
 // X, B, gamma, beta, eps, kind, alpha, gate, branch_gamma, mod_scale, mod_shift,
 // rows_per_group, h_out, image, codes, y
 PyObject* residual_norm_quant(PyObject* const* a) {
-    one_device(a, {{0, "X"}, {1, "B"}, {2, "gamma"}, {3, "beta"}, {7, "gate"}, {8, "branch_gamma"}, {9, "mod_scale"},
-                   {10, "mod_shift"}, {12, "h_out"}});
+    static constexpr Argument arguments[] = {{0, "X"}, {1, "B"}, {2, "gamma"}, {3, "beta"}, {7, "gate"},
+                                             {8, "branch_gamma"}, {9, "mod_scale"}, {10, "mod_shift"},
+                                             {12, "h_out", true}};
+    check_arguments(a, arguments);
     if (!THPVariable_Check(a[0]) || THPVariable_Unpack(a[0]).dim() != 2) value_error("X must be a [rows, width] tensor");
     const Tensor& x = THPVariable_Unpack(a[0]);
     const ScalarType type = x.scalar_type(), bf16 = ScalarType::BFloat16;
@@ -349,6 +377,7 @@ PyObject* residual_norm_quant(PyObject* const* a) {
         k, at_(y), static_cast<int8_t*>(at_(codes)), at_(image), static_cast<float*>(at_(sx)),
         c10::cuda::getCurrentCUDAStream().stream());
     if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
     return Py_BuildValue("(NNNNN)", wrap(h), wrap(image), wrap(sx), wrap(codes), wrap(y));
 }
 

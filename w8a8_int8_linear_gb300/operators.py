@@ -8,7 +8,9 @@ only checks its tensors, allocates outputs and passes pointers, sizes and the
 current stream to the library (include/w8a8.h states the arithmetic); here that
 is done in C++ (csrc/binding.cpp), as it would take longer than the kernels of
 single tokens.  Nothing synchronizes, so every call can be captured into a CUDA
-graph.
+graph.  Nothing is recorded for a backward pass; a tensor that is written in
+place (an output given, a cache) must not require a gradient outside
+torch.no_grad(), and autograd knows it as changed.
 """
 import importlib.machinery
 import importlib.util
