@@ -16,6 +16,7 @@
 #include "device_errors.h"
 #include "gemv.h"
 #include "kernels.h"
+#include "operators.h"
 
 namespace {
 

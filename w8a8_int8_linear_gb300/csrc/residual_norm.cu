@@ -31,7 +31,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "operators.h"
 #include "pair16.cuh"
 #include "ptx.cuh"
 #include "quant_core.cuh"

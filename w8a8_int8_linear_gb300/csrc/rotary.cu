@@ -18,7 +18,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "operators.h"
 #include "pair16.cuh"
 #include "ptx.cuh"
 
