@@ -77,7 +77,7 @@ def attention(Q, K, V, cu_q=None, cu_k=None, k_lens=None, batch=1, causal=True, 
 
 
 def rotary_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=None, fast=32.0, slow=1.0,
-                       device="cuda"):
+                       device="cuda", ramp="turns"):
     """Radians per position of each of the rot_dim / 2 pairs, fp64 [rot_dim / 2]:
     base ** (-2 k / rot_dim), for a context `factor` times longer than trained:
       "linear": all divided by factor;
@@ -85,12 +85,19 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original
                 slowest pair's frequency by factor and leaves the fastest;
       "yarn":   (Peng et al. 2023) pairs that turn more than `fast` times in
                 original_length positions are kept, those below `slow` turns
-                divided by factor, linearly in between; used with the
-                amplitude rotary_amplitude(factor) = 0.1 ln(factor) + 1."""
+                divided by factor, with a ramp in between; used with the
+                amplitude rotary_amplitude(factor) = 0.1 ln(factor) + 1.
+    "yarn" has two ramps, and a trained model needs its own (frequencies in between
+    differ by factors of up to 4).  ramp="turns" is the paper's formula, linear in
+    the number of turns; ramp="pairs" is linear in the pair's index, from the index
+    that has `fast` turns, rounded down, to the one that has `slow`, rounded up, as
+    in the authors' code and the models that follow it."""
     if rot_dim <= 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
     if scaling not in (None, "linear", "ntk", "yarn"):
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    if ramp not in ("turns", "pairs"):
+        raise ValueError("ramp must be 'turns' or 'pairs'")
     if not factor >= 1.0:
         raise ValueError("factor must be at least 1")
     k = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
@@ -102,9 +109,17 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original
     if scaling == "linear":
         f = f / factor
     elif scaling == "yarn":
-        if original_length is None or not fast > slow:
-            raise ValueError("'yarn' needs original_length, and fast > slow")
-        keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        if original_length is None or not fast > slow or (ramp == "pairs" and not slow > 0):
+            raise ValueError("'yarn' needs original_length, and fast > slow (above 0 with ramp='pairs')")
+        if ramp == "turns":
+            keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        else:
+            # original_length * base ** (-2 k / rot_dim) = 2 pi turns, solved for k
+            first, last = (rot_dim / 2 * math.log(original_length / (2 * math.pi * turns)) / math.log(base)
+                           for turns in (fast, slow))
+            first, last = max(math.floor(first), 0), min(math.ceil(last), rot_dim - 1)
+            pair = torch.arange(rot_dim // 2, dtype=torch.float64)
+            keep = 1 - ((pair - first) / max(last - first, 1e-3)).clamp(0, 1)
         f = f * keep + f / factor * (1 - keep)
     return f.to(device)
 
