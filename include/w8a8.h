@@ -385,8 +385,10 @@ typedef enum {
  * Rotary positions.  Pair k of every head of token t turns by the angle
  * a = positions[t] * freqs[k] (minus that with inverse, which is also the
  * gradient's direction): (x, y) -> amplitude * (x cos a - y sin a,
- * y cos a + x sin a).  Elements past the first rot of a head are copied.  The
- * angle is reduced exactly for any 64-bit position; cos and sin are binary32.
+ * y cos a + x sin a).  Elements past the first rot of a head are copied.  Whole
+ * turns are taken off the angle in 64-bit integers: it is off by at most
+ * 2^-63 |position| turns (4e-7 radians at 2^39, 8e-4 at 2^50; binary32, in which
+ * cos and sin are, resolves about 2e-7).
  *   Q [T,Hq,D], K [T,Hk,D] (NULL with Hk = 0), Q_out, K_out: dtype BF16 or
  *   FP16, last dimension dense, token and head strides in elements
  *   (multiples of 8, an output's not 0).  An output may be its input (same

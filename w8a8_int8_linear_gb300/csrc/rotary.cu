@@ -9,9 +9,10 @@
 //
 // The angle is held in turns as a 64-bit fraction: f_k / 2 pi as an integer
 // multiple of 2^-64 times the integer position, modulo 2^64, is the place on
-// the circle with the whole turns gone, off by 2^-64 p turns: a far position
-// costs nothing (binary32 p f_k is off by 2^-24 p f_k radians: 0.06 at
-// p = 10^6).  Its top 32 bits go to sincospif.
+// the circle with the whole turns gone, off by at most 2^-63 |p| turns (two
+// numbers cut to multiples of 2^-64): nothing beside binary32 up to p = 2^38
+// (binary32 p f_k is off by 2^-24 p f_k radians: 0.06 at p = 10^6).  Its top 32
+// bits go to sincospif.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
