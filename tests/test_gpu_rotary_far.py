@@ -30,3 +30,26 @@ def test_angle_bound(w8a8, bits):
     off = 6.3 * 2.0 ** -63 * torch.tensor([abs(p) for p in pos], dtype=torch.float64, device=DEV)[:, None]
     tol = off + 8e-7 + 2.0 ** -11 * want.abs() + 2.0 ** -25
     assert ((got[:, 0].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("bits", [0, 31, 40, 44, 50])
+def test_negative_frequencies_turn_back_as_far(w8a8, bits):
+    """(-p)(-f) = p f to the bit, and p (-f) = -(p f) within the bounds of two
+    calls (2^-32 of a turn each for the cut to 32 bits, then 8e-7 for binary32 and
+    half a step of the type), also for frequencies so slow that 1 - f / 2 pi has no
+    room for them."""
+    torch.manual_seed(bits)
+    x = torch.randn(6, 2, 16, device=DEV).to(torch.bfloat16)
+    pos = (1 << bits) + torch.arange(6, device=DEV) * 977
+    freqs = torch.tensor([1.0, 1e-2, 1e-3, 1e-5, 3e-7, 1e-9, 2.0 ** -20, 1e-12], dtype=torch.float64, device=DEV)
+    ahead, _ = w8a8.rotary(x, None, pos, freqs)
+    back, _ = w8a8.rotary(x, None, pos, freqs, inverse=True)
+    assert torch.equal(w8a8.rotary(x, None, -pos, -freqs)[0], ahead)
+    size = (x[..., :8].double().abs() + x[..., 8:].double().abs()).repeat(1, 1, 2)
+
+    def tol(want):
+        return 2 * (6.3 * 2.0 ** -32 + 8e-7) * size + 2 * 2.0 ** -8 * want.double().abs() * (1 + 2.0 ** -7)
+
+    for got, want in ((w8a8.rotary(x, None, pos, -freqs)[0], back),
+                      (w8a8.rotary(x, None, pos, -freqs, inverse=True)[0], ahead)):
+        assert ((got.double() - want.double()).abs() <= tol(want)).all()
