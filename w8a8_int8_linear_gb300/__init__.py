@@ -71,6 +71,7 @@ SIGNATURES = [
 ]
 
 _lib = None
+_several_gpus = False  # with one GPU there is no other for a tensor to be on
 
 
 class W8A8Error(RuntimeError):
@@ -84,7 +85,7 @@ class W8A8Error(RuntimeError):
 
 def lib():
     """Load the CUDA library (raises if it has not been built)."""
-    global _lib
+    global _lib, _several_gpus
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"W8A8 CUDA library not built ({LIB_PATH} missing): run __graft_entry__.build()")
@@ -93,6 +94,7 @@ def lib():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        _several_gpus = torch.cuda.device_count() > 1
         _lib = L
     return _lib
 
@@ -102,7 +104,13 @@ def _stream():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    if t is None:
+        return None
+    if _several_gpus and t.is_cuda and t.get_device() != torch.cuda.current_device():
+        # the kernels run on the current device
+        raise ValueError(f"a tensor is on cuda:{t.get_device()}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return ctypes.c_void_p(t.data_ptr())
 
 
 def _check(fn, status):
