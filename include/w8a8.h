@@ -398,7 +398,7 @@ typedef enum {
  * w8a8_rotary_append also copies V and writes K and V to rows slots[t] (int64,
  * device) of K_cache / V_cache [cache_rows,Hk,D]; a slot outside
  * [0, cache_rows) (-1 for a padding token) stores nothing.  Two tokens with
- * the same slot: either may win.
+ * the same slot: either may win, each 16 bytes for themselves.
  */
 W8A8_API w8a8_status w8a8_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
                                  int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token, int64_t q_head,
@@ -422,7 +422,8 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
  *   y  = n * (1 + mod_scale) + mod_shift
  *   sx[m] = max|y[m,:]| / 127, code = rne(y * (1 / sx[m])), at most 127 in size
  * in binary32 throughout: n is computed from the unrounded h and the codes
- * from the unrounded y.  The statistics are those of w8a8_norm_quant (both
+ * from the unrounded y (by a product with the reciprocal, so that a code next to
+ * a tie may differ by one from w8a8_quantize_act's division).  The statistics are those of w8a8_norm_quant (both
  * norms use eps); the quantizer's conventions for an all-zero row are those
  * of w8a8_quantize_act.  A row with a y that is not finite gets an sx that is
  * not finite (its codes then mean nothing), so that no finite numbers follow

@@ -661,9 +661,9 @@ size_t attention_workspace_bytes(int num_sms) {
 // Whether to split the keys over the CTAs rather than run the prompt kernel:
 // always up to one MMA tile of rows per sequence (the keys' bytes bound it) and
 // where there are no keys, which the split kernel runs without loading any;
-// above, by what a key costs.  The prompt kernel takes 7 ns a key for each wave
-// of items (a pair of 128-row tiles per SM), the split kernel 0.13 ns for each
-// block of 64 rows, and 2 us more around them.  Measured at 40 query heads on 8
+// above, by what a key costs.  The prompt kernel takes 7 to 11 ns a key for each
+// wave of items (a pair of 128-row tiles per SM), the split kernel 0.13 ns for each
+// block of 64 rows, and 2 us more around them; the rule takes 7.  Measured at 40 query heads on 8
 // KV heads x 128: 1 sequence x 64 queries over 32768 keys 202 us split against
 // 357, 4 x 8 over 32768 163 against 236, 4 x 16 293 against 236, 16 x 8 over
 // 4096 98 against 49, 1 x 4 over 512 13.7 against 11.3.

@@ -40,10 +40,11 @@
 // rate while key tiles stream (2900 clocks a pair of tiles).  An item costs about
 // 4000 clocks besides (the last softmax, the last product, O on its way out, 64 KB
 // at the 64 bytes a clock that an SM stores), and so do the causal tiles' unseen
-// half and the last wave.  Measured: 8192 tokens causal, 40 heads on 8 of 128, 434
-// us, 1580 TFLOP/s; 16384 x 8 heads full 650 us, 1690 TFLOP/s.  For D = 64 a key
-// tile's products take half as long and its softmax does not: 4096 x 32 heads full
-// 129 us, 1060 TFLOP/s.
+// half and the last wave.  Measured in bursts of 12 calls (2070 MHz): 8192 tokens
+// causal, 40 heads on 8 of 128, 435 us, 1580 TFLOP/s (in a longer loop, under the
+// power cap, 473 us, 1450); 16384 x 8 heads full 650 us, 1690 TFLOP/s.  For D = 64
+// a key tile's products take half as long and its softmax does not: 4096 x 32
+// heads full 129 to 136 us, 1010 to 1060 TFLOP/s.
 //
 // A weight of 0 does not hide a non-finite V (0 * inf = NaN).  In the key tiles
 // that some row does not see completely, warps 10-11 therefore replace the

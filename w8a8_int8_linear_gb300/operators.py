@@ -67,9 +67,10 @@ def attention(Q, K, V, cu_q=None, cu_k=None, k_lens=None, batch=1, causal=True, 
     sees all of its keys, the one before all but the last, and so on; a query
     that sees none gets zeros (lse: -inf).  scale: D ** -0.5.
 
-    Returns O [Tq, Hq, D], or (O, lse fp32 [Tq, Hq]) with lse=True.  The
-    workspace (`attention_workspace()`) is by default one per stream, and one
-    of its own for a captured call."""
+    Returns O [Tq, Hq, D], or (O, lse fp32 [Tq, Hq]) with lse=True.  `out`
+    must not overlap Q, K or V.  The workspace (`attention_workspace()`, 10 MB)
+    is by default one per stream, kept until the process ends, and one of its
+    own, in the graph's memory, for a captured call."""
     r = (_binding or binding()).attention(Q, K, V, cu_q, cu_k, k_lens, batch, causal, scale, out, lse, workspace)
     if type(r) is int:
         _check("w8a8_attention", r)
