@@ -415,6 +415,94 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
                                         w8a8_rotary_layout layout, void* stream);
 
 /*
+ * Norms of the heads of Q and K, then their rotary positions, in one pass:
+ * every head x [D] of token t becomes
+ *   y = x / sqrt(mean(x^2) + eps) * gamma          (kind RMS; LAYER: of x - mean(x))
+ * and pair k of y turns as in w8a8_rotary; in binary32 from the input to one
+ * rounding of the result.  A head whose squares leave binary32 (elements above
+ * 1.8e19, bf16 only) has no defined result.
+ *   q_gamma, k_gamma: the type of Q, [D], or a row for each head, q_gamma_head /
+ *   k_gamma_head elements apart (0: one row for all; a multiple of 8); NULL: 1.
+ *   Q, K, Q_out, K_out, positions, freqs, amplitude, layout: as in w8a8_rotary.
+ * w8a8_qk_norm_rotary_append also copies V and writes K and V to rows slots[t]
+ * (int64, device) of the caches: row r is row r % page_size of page
+ * r / page_size; pages of K_cache / V_cache lie kc_page / vc_page elements
+ * apart (multiples of 8), their rows kc_token / vc_token.  page_size 0: caches
+ * without pages.  A slot outside [0, cache_rows) stores nothing; two tokens
+ * with the same slot: either may win, each 16 bytes for themselves.
+ */
+W8A8_API w8a8_status w8a8_qk_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype,
+                                         int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token,
+                                         int64_t q_head, int64_t k_token, int64_t k_head, int64_t qo_token,
+                                         int64_t qo_head, int64_t ko_token, int64_t ko_head, const void* q_gamma,
+                                         int64_t q_gamma_head, const void* k_gamma, int64_t k_gamma_head, float eps,
+                                         w8a8_norm_kind kind, const int64_t* positions, const double* freqs,
+                                         float amplitude, w8a8_rotary_layout layout, void* stream);
+W8A8_API w8a8_status w8a8_qk_norm_rotary_append(
+    const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache, w8a8_dtype dtype, int64_t T,
+    int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t cache_rows, int64_t page_size, int64_t q_token,
+    int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head,
+    int64_t kc_page, int64_t kc_token, int64_t kc_head, int64_t vc_page, int64_t vc_token, int64_t vc_head,
+    const void* q_gamma, int64_t q_gamma_head, const void* k_gamma, int64_t k_gamma_head, float eps, w8a8_norm_kind kind,
+    const int64_t* positions, const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
+    void* stream);
+
+/*
+ * Attention of new tokens over a cache in pages: w8a8_attention where key j of
+ * sequence b is row j % page_size of page page_table[b * table_stride +
+ * j / page_size].
+ *   K_pages, V_pages [pages,page_size,Hk,D]: page, token and head strides in
+ *   elements (positive multiples of 8 below 2^39); page_size % 8 == 0, at most
+ *   2^20.
+ *   page_table [batch,max_pages] int32 (device), rows table_stride apart.  An
+ *   entry outside [0, pages) reads as a page of zeros; entries past the last
+ *   page of a sequence are not read.
+ *   k_lens [batch] int32 (device): keys of each sequence, its new tokens'
+ *   included (which are in the cache already); clamped to max_pages * page_size.
+ *   cu_q as in w8a8_attention.  max_queries: no sequence has more queries (0:
+ *   not known).  It only chooses between kernels: the result does not depend on
+ *   its being true.
+ *   workspace: w8a8_paged_attention_workspace_size() bytes, otherwise as in
+ *   w8a8_attention (the first w8a8_attention_workspace_zeroed() bytes zero
+ *   before its first use).
+ */
+W8A8_API size_t w8a8_paged_attention_workspace_size(void);
+W8A8_API w8a8_status w8a8_paged_attention(
+    const void* Q, const void* K_pages, const void* V_pages, void* O, float* lse, const int32_t* cu_q,
+    const int32_t* page_table, const int32_t* k_lens, w8a8_dtype dtype, int64_t batch, int64_t Tq, int64_t max_queries,
+    int64_t pages, int64_t page_size, int64_t max_pages, int64_t table_stride, int64_t Hq, int64_t Hk, int64_t D,
+    int64_t q_token, int64_t q_head, int64_t k_page, int64_t k_token, int64_t k_head, int64_t v_page, int64_t v_token,
+    int64_t v_head, int64_t o_token, int64_t o_head, float scale, int causal, void* workspace, size_t workspace_bytes,
+    void* stream);
+
+/*
+ * Pages of a cache, in all layers' caches at once.  caches[c] (n_caches of
+ * them, a host array of device pointers, 16-byte aligned) holds `pages` pages
+ * of page_bytes dense bytes (a multiple of 16), strides[c] bytes apart (a
+ * multiple of 16, at least page_bytes).
+ * w8a8_copy_pages: page dst[i] = page src[i] for i < n (int32, device).  A
+ * pair with an index outside [0, pages) copies nothing.  No page may be a
+ * destination twice, or a destination and a source (its contents would depend
+ * on the order of the copies).
+ * w8a8_fork_sequences: sequence dst[i] (a row of page_table [rows,max_pages],
+ * rows table_stride apart, and of k_lens [rows]; int32, device) becomes a
+ * second sequence like src[i] that can go on by itself: it gets its length and
+ * its full pages, and page new_pages[i] for what comes next, into which the
+ * last page is copied where it is only partly filled.  A length that fills
+ * every page of the row uses no new page.  Nothing happens where src[i] ==
+ * dst[i], or where one of the two rows or the new page is outside the table or
+ * the cache.  No row may be a destination twice, or a destination and a source;
+ * no new page may be used twice or belong to a sequence.  A row may be the
+ * source of many.
+ */
+W8A8_API w8a8_status w8a8_copy_pages(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
+                                     int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+W8A8_API w8a8_status w8a8_fork_sequences(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
+                                         int64_t page_bytes, int64_t page_size, int32_t* page_table, int64_t rows,
+                                         int64_t max_pages, int64_t table_stride, int32_t* k_lens, const int32_t* src,
+                                         const int32_t* dst, const int32_t* new_pages, int64_t n, void* stream);
+
+/*
  * From one block's output to the next block's W8A8 Linear in one pass:
  *   b' = B, or RMSNorm(B) * branch_gamma            (branch_gamma [K])
  *   h  = alpha * X + gate * b'                      (gate absent: 1)

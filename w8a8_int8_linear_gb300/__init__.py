@@ -57,6 +57,14 @@ SIGNATURES = [
     ("w8a8_attention", _I32, [_P] * 8 + [_I32] + [_I64] * 14 + [ctypes.c_float, _I32, _P, _SZ, _P]),
     ("w8a8_rotary", _I32, [_P] * 4 + [_I32] + [_I64] * 13 + [_P, _P, ctypes.c_float, _I32, _I32, _P]),
     ("w8a8_rotary_append", _I32, [_P] * 6 + [_I32] + [_I64] * 18 + [_P, _P, _P, ctypes.c_float, _I32, _P]),
+    ("w8a8_qk_norm_rotary", _I32, [_P] * 4 + [_I32] + [_I64] * 13 + [_P, _I64, _P, _I64, ctypes.c_float, _I32, _P, _P,
+                                                                    ctypes.c_float, _I32, _P]),
+    ("w8a8_qk_norm_rotary_append", _I32, [_P] * 6 + [_I32] + [_I64] * 21 +
+     [_P, _I64, _P, _I64, ctypes.c_float, _I32, _P, _P, _P, ctypes.c_float, _I32, _P]),
+    ("w8a8_paged_attention_workspace_size", _SZ, []),
+    ("w8a8_paged_attention", _I32, [_P] * 8 + [_I32] + [_I64] * 20 + [ctypes.c_float, _I32, _P, _SZ, _P]),
+    ("w8a8_copy_pages", _I32, [_P, _P, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    ("w8a8_fork_sequences", _I32, [_P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
     ("w8a8_residual_norm_quant", _I32, [_P, _P, _P, _I32] + [_P] * 6 + [_I64, _I64, ctypes.c_float, ctypes.c_float,
                                                                         _I32, _I64, _I64, _P, _P, _P, _P, _P]),
     ("w8a8_gemm_postscale_noalloc", _I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
@@ -537,7 +545,8 @@ def measure_imma_peak():
     return v.value
 
 
-from .operators import HALF, INTERLEAVED, attention, attention_workspace, residual_norm_quant, rotary, \
+from .operators import HALF, INTERLEAVED, attention, attention_workspace, copy_pages, fork_sequences, \
+    paged_attention, paged_attention_workspace, qk_norm_rotary, qk_norm_rotary_append, residual_norm_quant, rotary, \
     rotary_amplitude, rotary_append, rotary_frequencies  # noqa: E402
 from .module import Int8FFN, Int8Linear
 from .layer import Int8TransformerLayer  # noqa: E402

@@ -23,7 +23,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libw8a8_gb300.so")
 BINDING = os.path.join(OUT_DIR, f"w8a8_binding_torch{torch.__version__}.so")  # of this torch's C++ interface
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm_s8.cu", "gemv.cu", "norm.cu", "imma_peak.cu",
-           "attention.cu", "attention_prompt.cu", "rotary.cu", "residual_norm.cu"]
+           "attention.cu", "attention_prompt.cu", "attention_paged.cu", "rotary.cu", "norm_rotary.cu",
+           "residual_norm.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "--expt-relaxed-constexpr"]

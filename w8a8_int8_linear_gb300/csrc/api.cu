@@ -2,6 +2,7 @@
 // argument checks, device checks, workspace carving and kernel launches.
 // Every check runs before anything is enqueued, so a rejected call leaves
 // all outputs untouched.
+#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -682,16 +683,18 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
 
 namespace {
 
-// Checks and launch shared by the two rotary entry points.
-w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_layout layout, int64_t D, int64_t rot,
-                       cudaStream_t st) {
+// Checks shared by the rotary entry points; *none: there is nothing to do.
+w8a8_status check_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_layout layout, int64_t D, int64_t rot,
+                         bool* none) {
+    *none = false;
     if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
     if (layout != W8A8_ROTARY_HALF && layout != W8A8_ROTARY_INTERLEAVED) return W8A8_ERR_INVALID_ARG;
     if (a.tokens < 0 || a.cache_rows < 0 || a.q.heads < 0 || a.k.heads < 0 || D <= 0 || rot <= 0)
         return W8A8_ERR_INVALID_ARG;
     if (!(fabsf(a.amplitude) <= 3.0e38f)) return W8A8_ERR_INVALID_ARG;
     if (D % 8 != 0 || D > 256 || rot % 16 != 0 || rot > D || a.tokens > INT32_MAX) return W8A8_ERR_SHAPE;
-    if (a.tokens == 0 || (a.q.heads == 0 && a.k.heads == 0)) return W8A8_OK;
+    *none = a.tokens == 0 || (a.q.heads == 0 && a.k.heads == 0);
+    if (*none) return W8A8_OK;
     if (!a.positions || !a.freqs) return W8A8_ERR_INVALID_ARG;
     const w8a8::Heads* sides[6] = {&a.q, &a.q_out, &a.k, &a.k_out, &a.v, &a.v_out};
     for (const w8a8::Heads* h : sides) {
@@ -707,10 +710,79 @@ w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_
     if ((reinterpret_cast<uintptr_t>(a.positions) & 7u) || (reinterpret_cast<uintptr_t>(a.slots) & 7u) ||
         (reinterpret_cast<uintptr_t>(a.freqs) & 7u))
         return W8A8_ERR_ALIGNMENT;
+    return W8A8_OK;
+}
+
+w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_layout layout, int64_t D, int64_t rot,
+                       cudaStream_t st) {
+    bool none;
+    w8a8_status s = check_rotary(a, dtype, layout, D, rot, &none);
+    if (s != W8A8_OK || none) return s;
     DeviceInfo dev;
-    w8a8_status s = current_device(&dev);
-    if (s != W8A8_OK) return s;
+    if ((s = current_device(&dev)) != W8A8_OK) return s;
     return from_cuda(w8a8::launch_rotary(a, dtype, layout == W8A8_ROTARY_HALF, dev.num_sms, st), "rotary launch");
+}
+
+struct HeadNorms {
+    const void* q_gamma;
+    int64_t q_gamma_head;
+    const void* k_gamma;
+    int64_t k_gamma_head;
+    float eps;
+    w8a8_norm_kind kind;
+};
+
+w8a8_status run_norm_rotary(w8a8::NormRotaryArgs& a, const HeadNorms& n, w8a8_dtype dtype, w8a8_rotary_layout layout,
+                            int64_t D, int64_t rot, cudaStream_t st) {
+    if (n.kind != W8A8_NORM_RMS && n.kind != W8A8_NORM_LAYER) return W8A8_ERR_INVALID_ARG;
+    if (!(n.eps >= 0.0f)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
+    if (n.q_gamma_head < 0 || n.k_gamma_head < 0) return W8A8_ERR_INVALID_ARG;
+    bool none;
+    w8a8_status s = check_rotary(a.r, dtype, layout, D, rot, &none);
+    if (s != W8A8_OK || none) return s;
+    if (!aligned16(n.q_gamma) || !aligned16(n.k_gamma) || n.q_gamma_head % 8 != 0 || n.k_gamma_head % 8 != 0)
+        return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    if ((s = current_device(&dev)) != W8A8_OK) return s;
+    a.q_norm = {n.q_gamma, n.q_gamma_head};
+    a.k_norm = {n.k_gamma, n.k_gamma_head};
+    a.eps = n.eps;
+    a.layer = n.kind == W8A8_NORM_LAYER;
+    return from_cuda(w8a8::launch_norm_rotary(a, dtype, layout == W8A8_ROTARY_HALF, dev.num_sms, st),
+                     "head norm launch");
+}
+
+w8a8_status check_caches(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
+                         int64_t page_bytes) {
+    if (n_caches < 0 || pages < 0 || page_bytes <= 0) return W8A8_ERR_INVALID_ARG;
+    if (pages > INT32_MAX || page_bytes > (int64_t(1) << 32)) return W8A8_ERR_SHAPE;
+    if (n_caches > 0 && (!caches || !strides)) return W8A8_ERR_INVALID_ARG;
+    if (page_bytes % 16 != 0) return W8A8_ERR_ALIGNMENT;
+    for (int64_t i = 0; i < n_caches; ++i) {
+        if (pages > 0 && !caches[i]) return W8A8_ERR_INVALID_ARG;
+        if (!aligned16(caches[i]) || strides[i] % 16 != 0) return W8A8_ERR_ALIGNMENT;
+        if (pages > 1 && strides[i] < page_bytes) return W8A8_ERR_INVALID_ARG;  // on one another
+    }
+    return W8A8_OK;
+}
+
+// As many launches as the caches need.
+template <typename F>
+w8a8_status for_caches(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages, int64_t page_bytes,
+                       F launch) {
+    w8a8::PageCaches c{};
+    c.pages = static_cast<int>(pages);
+    c.page_bytes = page_bytes;
+    for (int64_t first = 0; first < n_caches; first += c.count) {
+        c.count = static_cast<int>(std::min<int64_t>(n_caches - first, w8a8::PageCaches::kMost));
+        for (int i = 0; i < c.count; ++i) {
+            c.base[i] = caches[first + i];
+            c.stride[i] = strides[first + i];
+        }
+        const w8a8_status s = from_cuda(launch(c, first == 0), "pages launch");
+        if (s != W8A8_OK) return s;
+    }
+    return W8A8_OK;
 }
 
 }  // namespace
@@ -766,6 +838,199 @@ w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void
     a.rot = static_cast<int>(rot);
     a.amplitude = amplitude;
     return run_rotary(a, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status w8a8_qk_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
+                                int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token, int64_t q_head,
+                                int64_t k_token, int64_t k_head, int64_t qo_token, int64_t qo_head, int64_t ko_token,
+                                int64_t ko_head, const void* q_gamma, int64_t q_gamma_head, const void* k_gamma,
+                                int64_t k_gamma_head, float eps, w8a8_norm_kind kind, const int64_t* positions,
+                                const double* freqs, float amplitude, w8a8_rotary_layout layout, void* stream) {
+    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
+    const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
+    w8a8::NormRotaryArgs a{};
+    a.r.q = {Q, q_token, q_head, hq};
+    a.r.q_out = {Q_out, qo_token, qo_head, hq};
+    a.r.k = {K, k_token, k_head, hk};
+    a.r.k_out = {K_out, ko_token, ko_head, hk};
+    a.r.positions = positions;
+    a.r.tokens = T;
+    a.r.freqs = freqs;
+    a.r.dim = static_cast<int>(D);
+    a.r.rot = static_cast<int>(rot);
+    a.r.amplitude = amplitude;
+    const HeadNorms n = {q_gamma, q_gamma_head, k_gamma, k_gamma_head, eps, kind};
+    return run_norm_rotary(a, n, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status w8a8_qk_norm_rotary_append(
+    const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache, w8a8_dtype dtype, int64_t T,
+    int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t cache_rows, int64_t page_size, int64_t q_token,
+    int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head,
+    int64_t kc_page, int64_t kc_token, int64_t kc_head, int64_t vc_page, int64_t vc_token, int64_t vc_head,
+    const void* q_gamma, int64_t q_gamma_head, const void* k_gamma, int64_t k_gamma_head, float eps, w8a8_norm_kind kind,
+    const int64_t* positions, const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
+    void* stream) {
+    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
+    if (Hk <= 0 || page_size < 0) return W8A8_ERR_INVALID_ARG;
+    if (T > 0 && !slots) return W8A8_ERR_INVALID_ARG;
+    if (page_size > INT32_MAX) return W8A8_ERR_SHAPE;
+    if (page_size > 0) {
+        if (kc_page < 0 || vc_page < 0 || kc_page % 8 != 0 || vc_page % 8 != 0) return W8A8_ERR_ALIGNMENT;
+        if ((kc_page == 0 || vc_page == 0) && cache_rows > page_size) return W8A8_ERR_INVALID_ARG;  // on one another
+    }
+    const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
+    w8a8::NormRotaryArgs a{};
+    a.r.q = {Q, q_token, q_head, hq};
+    a.r.q_out = {Q_out, qo_token, qo_head, hq};
+    a.r.k = {K, k_token, k_head, hk};
+    a.r.k_out = {K_cache, kc_token, kc_head, hk};
+    a.r.v = {V, v_token, v_head, hk};
+    a.r.v_out = {V_cache, vc_token, vc_head, hk};
+    a.r.positions = positions;
+    a.r.slots = slots;
+    a.r.tokens = T;
+    a.r.cache_rows = cache_rows;
+    a.r.freqs = freqs;
+    a.r.dim = static_cast<int>(D);
+    a.r.rot = static_cast<int>(rot);
+    a.r.amplitude = amplitude;
+    a.page_size = page_size;
+    a.k_page = kc_page;
+    a.v_page = vc_page;
+    const HeadNorms n = {q_gamma, q_gamma_head, k_gamma, k_gamma_head, eps, kind};
+    return run_norm_rotary(a, n, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+size_t w8a8_paged_attention_workspace_size(void) {
+    DeviceInfo dev;
+    return current_device(&dev) == W8A8_OK ? w8a8::paged_attention_workspace_bytes(dev.num_sms) : 0;
+}
+
+w8a8_status w8a8_paged_attention(
+    const void* Q, const void* K_pages, const void* V_pages, void* O, float* lse, const int32_t* cu_q,
+    const int32_t* page_table, const int32_t* k_lens, w8a8_dtype dtype, int64_t batch, int64_t Tq, int64_t max_queries,
+    int64_t pages, int64_t page_size, int64_t max_pages, int64_t table_stride, int64_t Hq, int64_t Hk, int64_t D,
+    int64_t q_token, int64_t q_head, int64_t k_page, int64_t k_token, int64_t k_head, int64_t v_page, int64_t v_token,
+    int64_t v_head, int64_t o_token, int64_t o_head, float scale, int causal, void* workspace, size_t workspace_bytes,
+    void* stream) {
+    if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return W8A8_ERR_INVALID_ARG;
+    if (batch < 0 || Tq < 0 || max_queries < 0 || pages < 0 || page_size <= 0 || max_pages < 0 || table_stride < 0 ||
+        Hq <= 0 || Hk <= 0 || D <= 0)
+        return W8A8_ERR_INVALID_ARG;
+    const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;  // the kernels' exponentials are 2^x
+    if (!(scale > 0.0f) || !(scale_log2 <= 3.4e38)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
+    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || batch > INT32_MAX ||
+        Tq * (Hq / Hk) > INT32_MAX)
+        return W8A8_ERR_SHAPE;
+    if (page_size % 8 != 0 || page_size > (1 << 20) || pages >= INT32_MAX || max_pages > INT32_MAX / page_size ||
+        table_stride > INT32_MAX)
+        return W8A8_ERR_SHAPE;
+    if (batch == 0 || Tq == 0) return W8A8_OK;
+    if (!cu_q && Tq % batch != 0) return W8A8_ERR_SHAPE;
+    if (!Q || !O || !k_lens || (max_pages > 0 && !page_table) || (pages > 0 && (!K_pages || !V_pages)))
+        return W8A8_ERR_INVALID_ARG;
+    const int64_t strides[10] = {q_token, q_head, k_page, k_token, k_head, v_page, v_token, v_head, o_token, o_head};
+    for (int64_t v : strides)
+        if (v <= 0 || v >= (int64_t(1) << 39) || v % 8 != 0) return W8A8_ERR_ALIGNMENT;
+    if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) || !aligned4(lse) ||
+        !aligned4(cu_q) || !aligned4(page_table) || !aligned4(k_lens))
+        return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    w8a8_status s = current_device(&dev);
+    if (s != W8A8_OK) return s;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < w8a8::paged_attention_workspace_bytes(dev.num_sms))
+        return W8A8_ERR_WORKSPACE;
+    w8a8::AttentionArgs a{};
+    a.q = Q;
+    a.k = K_pages;
+    a.v = V_pages;
+    a.o = O;
+    a.lse = lse;
+    a.cu_q = cu_q;
+    a.k_lens = k_lens;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.k_page = k_page;
+    a.v_page = v_page;
+    a.pages = static_cast<int>(pages);
+    a.page_size = static_cast<int>(page_size);
+    a.max_pages = pages > 0 ? static_cast<int>(max_pages) : 0;  // a cache of no pages has no keys
+    a.batch = static_cast<int>(batch);
+    a.Tq = static_cast<int>(Tq);
+    a.Hq = static_cast<int>(Hq);
+    a.Hk = static_cast<int>(Hk);
+    a.D = static_cast<int>(D);
+    a.group = static_cast<int>(Hq / Hk);
+    a.q_token = q_token;
+    a.q_head = q_head;
+    a.k_token = k_token;
+    a.k_head = k_head;
+    a.v_token = v_token;
+    a.v_head = v_head;
+    a.o_token = o_token;
+    a.o_head = o_head;
+    a.scale_log2 = static_cast<float>(scale_log2);
+    a.causal = causal != 0;
+    int64_t most = cu_q ? Tq : Tq / batch;
+    if (max_queries > 0 && max_queries < most) most = max_queries;
+    void* enc = encode_fn();
+    if (!enc) return W8A8_ERR_CUDA;
+    t_detail[0] = 0;
+    const cudaError_t e = w8a8::launch_paged_attention(a, static_cast<int>(most), dtype, dev.num_sms, workspace, enc,
+                                                       static_cast<cudaStream_t>(stream), t_detail, sizeof t_detail);
+    if (e == cudaSuccess) return W8A8_OK;
+    cudaGetLastError();
+    return t_detail[0] ? W8A8_ERR_CUDA : cuda_fail("paged attention launch", e);
+}
+
+w8a8_status w8a8_copy_pages(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
+                            int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+    if (n < 0) return W8A8_ERR_INVALID_ARG;
+    w8a8_status s = check_caches(caches, strides, n_caches, pages, page_bytes);
+    if (s != W8A8_OK) return s;
+    if (n == 0 || n_caches == 0 || pages == 0) return W8A8_OK;
+    if (!src || !dst) return W8A8_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst)) return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    if ((s = current_device(&dev)) != W8A8_OK) return s;
+    return for_caches(caches, strides, n_caches, pages, page_bytes, [&](const w8a8::PageCaches& c, bool) {
+        return w8a8::launch_copy_pages(c, src, dst, n, static_cast<cudaStream_t>(stream));
+    });
+}
+
+w8a8_status w8a8_fork_sequences(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
+                                int64_t page_bytes, int64_t page_size, int32_t* page_table, int64_t rows,
+                                int64_t max_pages, int64_t table_stride, int32_t* k_lens, const int32_t* src,
+                                const int32_t* dst, const int32_t* new_pages, int64_t n, void* stream) {
+    if (n < 0 || rows < 0 || max_pages < 0 || page_size <= 0 || table_stride < 0) return W8A8_ERR_INVALID_ARG;
+    w8a8_status s = check_caches(caches, strides, n_caches, pages, page_bytes);
+    if (s != W8A8_OK) return s;
+    if (rows > INT32_MAX || page_size > INT32_MAX || max_pages > INT32_MAX / page_size || table_stride > INT32_MAX)
+        return W8A8_ERR_SHAPE;
+    if (n == 0 || n_caches == 0 || pages == 0 || rows == 0) return W8A8_OK;
+    if (!k_lens || !src || !dst || !new_pages || (max_pages > 0 && !page_table)) return W8A8_ERR_INVALID_ARG;
+    if (table_stride < max_pages && rows > 1) return W8A8_ERR_INVALID_ARG;
+    if (!aligned4(page_table) || !aligned4(k_lens) || !aligned4(src) || !aligned4(dst) || !aligned4(new_pages))
+        return W8A8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    if ((s = current_device(&dev)) != W8A8_OK) return s;
+    w8a8::ForkArgs f{};
+    f.table = page_table;
+    f.table_stride = table_stride;
+    f.k_lens = k_lens;
+    f.src = src;
+    f.dst = dst;
+    f.page = new_pages;
+    f.n = n;
+    f.rows = static_cast<int>(rows);
+    f.max_pages = static_cast<int>(max_pages);
+    f.page_size = static_cast<int>(page_size);
+    return for_caches(caches, strides, n_caches, pages, page_bytes, [&](const w8a8::PageCaches& c, bool first) {
+        f.tables = first;
+        return w8a8::launch_fork_sequences(c, f, static_cast<cudaStream_t>(stream));
+    });
 }
 
 w8a8_status w8a8_residual_norm_quant(const void* X, const void* B, void* H, w8a8_dtype x_dtype,

@@ -33,7 +33,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdio>
+#include <numeric>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -103,12 +105,12 @@ __device__ __forceinline__ int tiles_of(const Sequence& s) { return max(1, (s.m 
 
 // Tiles of the 32 sequences from b0 on: this lane's, and inclusive over the
 // lanes; `most` becomes the most of one item.
-template <int R>
+template <int R, bool kPaged>
 __device__ __forceinline__ void tiles_from(const AttentionArgs& p, int b0, int64_t& mine, int64_t& incl, int& most) {
     const int lane = threadIdx.x & 31;
     mine = 0;
     if (b0 + lane < p.batch) {
-        const Sequence s = sequence(p, b0 + lane);
+        const Sequence s = sequence<kPaged>(p, b0 + lane);
         mine = static_cast<int64_t>(blocks_of<R>(p, s)) * (p.Hk / p.side_heads) * tiles_of(s);
         most = max(most, tiles_of(s));
     }
@@ -132,7 +134,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
-template <typename T, int DP, int R, int G>
+template <typename T, int DP, int R, int G, bool kPaged>
 __global__ void __launch_bounds__(threads_of(G), 3 - G)
     attention_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const AttentionArgs p) {
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     const int side = blockIdx.x % p.side_heads, range = blockIdx.x / p.side_heads, ranges = gridDim.x / p.side_heads;
     const int head_groups = p.Hk / p.side_heads;
     Sequence own = {0, 0, 0, 0};  // this lane's, of up to 32
-    if (p.batch <= 32 && lane < p.batch) own = sequence(p, lane);
+    if (p.batch <= 32 && lane < p.batch) own = sequence<kPaged>(p, lane);
     const int blocks = blocks_of<R>(p, own), items = blocks * head_groups, tiles = tiles_of(own);
     int64_t mine = static_cast<int64_t>(items) * tiles, incl, total;
     int most = tiles;
@@ -174,11 +176,11 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     if (few) {
         total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine));
     } else {
-        tiles_from<R>(p, 0, mine, incl, most);
+        tiles_from<R, kPaged>(p, 0, mine, incl, most);
         total = __shfl_sync(0xffffffffu, incl, 31);
         for (int b0 = 32; b0 < p.batch; b0 += 32) {
             int64_t m2, i2;
-            tiles_from<R>(p, b0, m2, i2, most);
+            tiles_from<R, kPaged>(p, b0, m2, i2, most);
             total += __shfl_sync(0xffffffffu, i2, 31);
         }
     }
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     {  // the cursor of tile w
         int64_t left = w;
         for (int b0 = 0;; b0 += 32) {
-            if (b0 > 0) tiles_from<R>(p, b0, mine, incl, most);
+            if (b0 > 0) tiles_from<R, kPaged>(p, b0, mine, incl, most);
             const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
             if (hit) {
                 const int l = __ffs(hit) - 1;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
             c.tiles = of(tiles);
             line = of(line);
         } else {
-            c.s = sequence(p, c.b);
+            c.s = sequence<kPaged>(p, c.b);
             c.blocks = blocks_of<R>(p, c.s);
             line = c.tiles = tiles_of(c.s);
         }
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
             c.item = 0;
             do {
                 if (++c.b >= p.batch) return false;
-                c.s = sequence(p, c.b);
+                c.s = sequence<kPaged>(p, c.b);
                 c.blocks = blocks_of<R>(p, c.s);
                 c.tiles = tiles_of(c.s);
             } while (c.blocks == 0);
@@ -291,10 +293,32 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
         for (bool more = true; more && ok;) {
             const int t_end = piece_end(), hg = c.item / c.blocks, rb = c.item - hg * c.blocks;
             const int end = seen_end(rb, t_end), hk = hg * p.side_heads + side;
+            // keys in pages: lane i fetches the tile's box i, from the page that it looked up
+            // while the tile before was waited for
+            const auto look_up = [&](int t) {
+                const int key = t * kTile + lane * p.box;
+                return key < min(c.s.m, (t + 1) * kTile) ? page_of(p, c.b, key) : p.pages;
+            };
+            int page = kPaged && c.tile < end ? look_up(c.tile) : 0;
             for (int t = c.tile; t < end; ++t) {
+                const int next_page = kPaged && t + 1 < end ? look_up(t + 1) : 0;
                 ok = mbar_wait(&empty[st], ph ^ 1, 50);
                 if (!ok) break;
-                if (elect_one_sync()) {
+                if (kPaged) {
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kStage);
+                    __syncwarp();
+                    if (lane * p.box < kTile) {
+                        const int key = t * kTile + lane * p.box, row = key % p.page_size;
+                        const uint32_t dst = smem_u32(smem) + st * L::kStage + lane * p.box * 128;
+#pragma unroll
+                        for (int x = 0; x < DP / 64; ++x) {
+                            tma_load_page(dst + x * L::kChunk, &tmK, &full[st], 64 * x, hk, row, page);
+                            tma_load_page(dst + L::kKv + x * L::kChunk, &tmV, &full[st], 64 * x, hk, row, page);
+                        }
+                    }
+                    __syncwarp();
+                    page = next_page;
+                } else if (elect_one_sync()) {
                     mbar_arrive_expect_tx(&full[st], L::kStage);
                     const uint32_t dst = smem_u32(smem) + st * L::kStage;
 #pragma unroll
@@ -605,27 +629,27 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     }
 }
 
-template <typename T, int DP, int R, int G>
+template <typename T, int DP, int R, int G, bool kPaged>
 cudaError_t launch_split_rows(const CUtensorMap (&map)[2], const AttentionArgs& a, int num_sms, cudaStream_t st) {
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R, G, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SplitSmem<DP, R, G>::kTotal);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
     const int ctas = (3 - G) * num_sms / a.side_heads * a.side_heads;
-    attention_split_kernel<T, DP, R, G><<<ctas, threads_of(G), SplitSmem<DP, R, G>::kTotal, st>>>(map[0], map[1], a);
+    attention_split_kernel<T, DP, R, G, kPaged><<<ctas, threads_of(G), SplitSmem<DP, R, G>::kTotal, st>>>(map[0], map[1], a);
     return cudaGetLastError();
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kPaged>
 cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, int num_sms, cudaStream_t st) {
     // as many rows an item as a sequence has, so that its keys are read once
-    const int64_t rows = static_cast<int64_t>(a.Tq) * a.group;
+    const int64_t rows = kPaged ? a.expected_rows * static_cast<int64_t>(a.batch) : static_cast<int64_t>(a.Tq) * a.group;
     if (rows <= 16 * static_cast<int64_t>(a.batch)) {
         // Two CTAs per SM where they get several items each: one starts and ends an
         // item while the other's keys stream (us, against one CTA, at heads of 128, 8
@@ -634,11 +658,21 @@ cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, in
         // into twice as many pieces (16 of 8192 86 against 84, on 1 KV head 27 against
         // 24, 4 of 500 9.8 against 9.5).
         const int64_t items = static_cast<int64_t>(a.batch) * (a.Hk / a.side_heads);
-        if (2 * items >= 3 * (num_sms / a.side_heads)) return launch_split_rows<T, DP, 16, 1>(map, a, num_sms, st);
-        return launch_split_rows<T, DP, 16, 2>(map, a, num_sms, st);
+        if (2 * items >= 3 * (num_sms / a.side_heads)) return launch_split_rows<T, DP, 16, 1, kPaged>(map, a, num_sms, st);
+        return launch_split_rows<T, DP, 16, 2, kPaged>(map, a, num_sms, st);
     }
-    if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32, 2>(map, a, num_sms, st);
-    return launch_split_rows<T, DP, 64, 2>(map, a, num_sms, st);
+    if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32, 2, kPaged>(map, a, num_sms, st);
+    return launch_split_rows<T, DP, 64, 2, kPaged>(map, a, num_sms, st);
+}
+
+template <bool kPaged>
+cudaError_t launch_split_typed(const CUtensorMap (&map)[2], const AttentionArgs& a, int dtype, int num_sms,
+                               cudaStream_t st) {
+    if (dtype == kBf16)
+        return a.D <= 64 ? launch_split<__nv_bfloat16, 64, kPaged>(map, a, num_sms, st)
+                         : launch_split<__nv_bfloat16, 128, kPaged>(map, a, num_sms, st);
+    return a.D <= 64 ? launch_split<__half, 64, kPaged>(map, a, num_sms, st)
+                     : launch_split<__half, 128, kPaged>(map, a, num_sms, st);
 }
 
 // Heads that run side by side: the largest divisor of Hk up to 8.
@@ -693,6 +727,25 @@ cudaError_t encode_heads(void* encode_fn, CUtensorMap* map, char name, const voi
     return cudaErrorInvalidValue;
 }
 
+cudaError_t encode_pages(void* encode_fn, CUtensorMap* map, char name, const void* ptr, int dtype, int pages,
+                         int page_size, int heads, int dim, int64_t page, int64_t token, int64_t head, int box_rows,
+                         char* detail, size_t n) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                          static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(pages)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2,
+                             static_cast<cuuint64_t>(page) * 2};
+    cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode_fn)(
+        map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+        const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return cudaSuccess;
+    snprintf(detail, n, "cuTensorMapEncodeTiled(%c: %d pages of %d x %d x %d) returned %d", name, pages, page_size, heads,
+             dim, static_cast<int>(r));
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num_sms, void* workspace, void* encode_fn,
                                    cudaStream_t st, char* detail, size_t n) {
     AttentionArgs a = args;
@@ -703,6 +756,19 @@ cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num
     const int64_t rows = (static_cast<int64_t>(a.Tq) * a.group + a.batch - 1) / a.batch;
     a.join_rounds = static_cast<int>(((rows < 64 ? rows : 64) * (a.D <= 64 ? 16 : 32) + 255) / 256);
     CUtensorMap map[2] = {};  // without keys, nothing is loaded
+    if (a.page_table) {
+        a.join_rounds = (std::min(a.expected_rows, 64) * (a.D <= 64 ? 16 : 32) + 255) / 256;
+        a.box = std::gcd(a.page_size, kTile);
+        if (a.max_pages > 0) {
+            cudaError_t e = encode_pages(encode_fn, &map[0], 'K', a.k, dtype, a.pages, a.page_size, a.Hk, a.D, a.k_page,
+                                         a.k_token, a.k_head, a.box, detail, n);
+            if (e == cudaSuccess)
+                e = encode_pages(encode_fn, &map[1], 'V', a.v, dtype, a.pages, a.page_size, a.Hk, a.D, a.v_page,
+                                 a.v_token, a.v_head, a.box, detail, n);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_split_typed<true>(map, a, dtype, num_sms, st);
+    }
     if (a.Tk > 0) {
         cudaError_t e = encode_heads(encode_fn, &map[0], 'K', a.k, dtype, a.Tk, a.Hk, a.D, a.k_token, a.k_head, 1,
                                      kTile, detail, n);
@@ -711,10 +777,7 @@ cudaError_t launch_attention_split(const AttentionArgs& args, int dtype, int num
                              detail, n);
         if (e != cudaSuccess) return e;
     }
-    if (dtype == kBf16)
-        return a.D <= 64 ? launch_split<__nv_bfloat16, 64>(map, a, num_sms, st)
-                         : launch_split<__nv_bfloat16, 128>(map, a, num_sms, st);
-    return a.D <= 64 ? launch_split<__half, 64>(map, a, num_sms, st) : launch_split<__half, 128>(map, a, num_sms, st);
+    return launch_split_typed<false>(map, a, dtype, num_sms, st);
 }
 
 cudaError_t attention_split_read_device_error(unsigned int* code) {

@@ -31,6 +31,7 @@ struct Sequence {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
+template <bool kPaged = false>
 __device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
     Sequence s;
     if (p.cu_q) {
@@ -39,6 +40,13 @@ __device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
     } else {
         s.n = p.Tq / p.batch;
         s.q0 = b * s.n;
+    }
+    if (kPaged) {
+        const int64_t rows = static_cast<int64_t>(s.n) * p.group;
+        if (rows <= p.few_rows || rows > p.most_rows) s.n = 0;  // another launch's
+        s.k0 = 0;
+        s.m = clampi(p.k_lens[b], 0, p.max_pages * p.page_size);
+        return s;
     }
     if (p.cu_k) {
         s.k0 = clampi(p.cu_k[b], 0, p.Tk);
@@ -58,6 +66,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap,
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// The page of key `key` of sequence b, for a key below its length; one that is not in
+// the cache comes as `pages`, where copies read zeros.
+__device__ __forceinline__ int page_of(const AttentionArgs& p, int b, int key) {
+    const unsigned page = static_cast<unsigned>(
+        __ldg(p.page_table + static_cast<int64_t>(b) * p.table_stride + static_cast<unsigned>(key) / static_cast<unsigned>(p.page_size)));
+    return static_cast<int>(min(page, static_cast<unsigned>(p.pages)));
+}
+
+// The same from pages: a box of one page.
+__device__ __forceinline__ void tma_load_page(uint32_t smem_dst, const void* tmap, uint64_t* bar, int32_t c0,
+                                              int32_t head, int32_t row, int32_t page) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(head), "r"(row), "r"(page)
         : "memory");
 }
 

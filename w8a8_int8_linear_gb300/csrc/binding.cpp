@@ -18,6 +18,7 @@
 #include <map>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/w8a8.h"
 
@@ -168,19 +169,21 @@ PyObject* wrap(const Tensor& t) {
 PyObject* status(w8a8_status s) { return PyLong_FromLong(s); }
 
 // A new workspace, its counters zeroed on the current stream.
-Tensor new_workspace(const Tensor& like) {
-    Tensor ws = at::empty({static_cast<int64_t>(w8a8_attention_workspace_size())}, like.options().dtype(ScalarType::Byte));
+Tensor new_workspace(const Tensor& like, size_t size) {
+    Tensor ws = at::empty({static_cast<int64_t>(size)}, like.options().dtype(ScalarType::Byte));
     ws.narrow(0, 0, static_cast<int64_t>(w8a8_attention_workspace_zeroed())).zero_();
     return ws;
 }
 
 // One per stream; a captured call gets its own, zeroed by every replay.
+template <size_t (*size)()>
 Tensor workspace_of(const Tensor& like, cudaStream_t stream) {
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return new_workspace(like);
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+        return new_workspace(like, size());
     // not freed at exit, when the CUDA context may be gone before it
     static auto* all = new std::map<std::pair<int, cudaStream_t>, Tensor>;
     Tensor& ws = (*all)[{like.get_device(), stream}];
-    if (!ws.defined()) ws = new_workspace(like);
+    if (!ws.defined()) ws = new_workspace(like, size());
     return ws;
 }
 
@@ -215,12 +218,91 @@ PyObject* attention(PyObject* const* a) {
     const Heads ho = output(a[9], "out", q, hq, type, out);
     if (truth(a[10])) lse = empty({hq.tokens, hq.heads}, ScalarType::Float, q);
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream().stream();
-    const Tensor ws = none(a[11]) ? workspace_of(q, stream) : tensor(a[11], "workspace");
+    const Tensor ws = none(a[11]) ? workspace_of<w8a8_attention_workspace_size>(q, stream) : tensor(a[11], "workspace");
     if (!ws.is_cuda() || !ws.is_contiguous()) value_error("workspace must be a dense CUDA tensor");
     const w8a8_status s = w8a8_attention(
         hq.ptr, hk.ptr, hv.ptr, ho.ptr, lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, cu_q, cu_k, k_lens,
         dtype_of(type), batch, hq.tokens, hk.tokens, hq.heads, hk.heads, hq.dim, hq.token, hq.head, hk.token, hk.head,
         hv.token, hv.head, ho.token, ho.head, static_cast<float>(scale), truth(a[7]), ws.data_ptr(), ws.nbytes(), stream);
+    if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
+    if (!lse.defined()) return wrap(out);
+    return Py_BuildValue("(NN)", wrap(out), wrap(lse));
+}
+
+// A cache in pages, [pages, page_size, KV heads, dim], or rows [rows, KV heads, dim]
+// (page_size 0); otherwise like a [tokens, heads, dim] tensor.
+struct Cache {
+    void* ptr;
+    int64_t pages, page_size, heads, dim, page, token, head;
+};
+Cache cache(const Tensor& t, const char* name, ScalarType type, bool rows_too) {
+    const std::string n(name);
+    if (rows_too && t.dim() == 3) {
+        const Heads h = heads(t, name, &type);
+        return {h.ptr, h.tokens, 0, h.heads, h.dim, 0, h.token, h.head};
+    }
+    if (t.scalar_type() != type) type_error(n + " must be " + name_of(type) + ", got " + name_of(t.scalar_type()));
+    if (!t.is_cuda()) value_error(n + " must be a CUDA tensor");
+    if (t.dim() != 4)
+        value_error(n + " must be [pages, page_size, KV heads, dim]" + (rows_too ? " or [rows, KV heads, dim]" : ""));
+    const auto size = t.sizes(), stride = t.strides();
+    if (stride[3] != 1 && size[3] != 1) value_error(n + " must be dense in its last dimension");
+    const int64_t token = size[1] != 1 ? stride[1] : size[2] * size[3];
+    return {t.data_ptr(), size[0], size[1], size[2], size[3], size[0] != 1 ? stride[0] : size[1] * size[2] * size[3],
+            token, size[2] != 1 ? stride[2] : size[3]};
+}
+
+// An int32 [rows, columns] tensor on the GPU, dense in its last dimension.
+struct Table {
+    int32_t* ptr;
+    int64_t rows, columns, stride;
+};
+Table table(PyObject* o, const char* name) {
+    const std::string n(name);
+    if (!THPVariable_Check(o) || THPVariable_Unpack(o).scalar_type() != ScalarType::Int)
+        type_error(n + " must be a torch.int32 tensor");
+    const Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
+        value_error(n + " must be a CUDA tensor [sequences, pages], dense in its last dimension");
+    return {static_cast<int32_t*>(t.data_ptr()), t.size(0), t.size(1), t.size(0) != 1 ? t.stride(0) : t.size(1)};
+}
+
+// Q, k_pages, v_pages, page_table, k_lens, cu_q, max_queries, causal, scale, out, lse, workspace
+PyObject* paged_attention(PyObject* const* a) {
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "k_pages"}, {2, "v_pages"}, {3, "page_table"}, {4, "k_lens"},
+                                             {5, "cu_q"}, {9, "out", true}, {11, "workspace"}};
+    check_arguments(a, arguments);
+    Tensor q = tensor(a[0], "Q");
+    const Tensor &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages");
+    Heads hq = heads(q, "Q");
+    const ScalarType type = q.scalar_type();
+    const Cache ck = cache(k, "k_pages", type, false), cv = cache(v, "v_pages", type, false);
+    if (!(hq.token && hq.head)) {  // a broadcast dimension is laid out
+        q = q.contiguous();
+        hq = heads(q, "Q");
+    }
+    if (ck.dim != hq.dim || k.sizes() != v.sizes())
+        value_error("k_pages and v_pages must be [pages, page_size, KV heads, dim] with the queries' dim");
+    const Table pt = table(a[3], "page_table");
+    const auto* k_lens = indices<int32_t>(a[4], ScalarType::Int, pt.rows, "k_lens");
+    const auto* cu_q = none(a[5]) ? nullptr : indices<int32_t>(a[5], ScalarType::Int, pt.rows + 1, "cu_q");
+    const int64_t most = none(a[6]) ? 0 : integer(a[6]);
+    if (most < 0) value_error("max_queries must not be negative");
+    const double scale = none(a[8]) ? 1.0 / std::sqrt(static_cast<double>(hq.dim)) : number(a[8]);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Tensor out, lse;
+    const Heads ho = output(a[9], "out", q, hq, type, out);
+    if (truth(a[10])) lse = empty({hq.tokens, hq.heads}, ScalarType::Float, q);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream().stream();
+    const Tensor ws =
+        none(a[11]) ? workspace_of<w8a8_paged_attention_workspace_size>(q, stream) : tensor(a[11], "workspace");
+    if (!ws.is_cuda() || !ws.is_contiguous()) value_error("workspace must be a dense CUDA tensor");
+    const w8a8_status s = w8a8_paged_attention(
+        hq.ptr, ck.ptr, cv.ptr, ho.ptr, lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, cu_q, pt.ptr,
+        k_lens, dtype_of(type), pt.rows, hq.tokens, most, ck.pages, ck.page_size, pt.columns, pt.stride, hq.heads, ck.heads,
+        hq.dim, hq.token, hq.head, ck.page, ck.token, ck.head, cv.page, cv.token, cv.head, ho.token, ho.head,
+        static_cast<float>(scale), truth(a[7]), ws.data_ptr(), ws.nbytes(), stream);
     if (s != W8A8_OK) return status(s);
     bump_written(a, arguments);
     if (!lse.defined()) return wrap(out);
@@ -297,6 +379,189 @@ PyObject* rotary_append(PyObject* const* a) {
     if (s != W8A8_OK) return status(s);
     bump_written(a, arguments);
     return wrap(q_out);
+}
+
+// gamma [dim] or [heads, dim] of the heads' type; null for None.
+struct Gamma {
+    const void* ptr = nullptr;
+    int64_t head = 0;
+};
+Gamma gamma_of(PyObject* o, const char* name, ScalarType type, const Heads& h) {
+    if (none(o)) return {};
+    const std::string n(name);
+    const Tensor& t = tensor(o, name);
+    if (t.scalar_type() != type) type_error(n + " must be " + name_of(type) + ", got " + name_of(t.scalar_type()));
+    const int64_t d = t.dim();
+    if (!t.is_cuda() || d < 1 || d > 2 || t.size(d - 1) != h.dim || (d == 2 && t.size(0) != h.heads) ||
+        (t.stride(d - 1) != 1 && h.dim != 1))
+        value_error(n + " must be a CUDA tensor [dim] or [heads, dim], dense in its last dimension");
+    return {t.data_ptr(), d == 2 && h.heads != 1 ? t.stride(0) : 0};
+}
+
+// Q, K, positions, freqs, q_gamma, k_gamma, eps, kind, layout, amplitude, q_out, k_out
+PyObject* qk_norm_rotary(PyObject* const* a) {
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "K"}, {2, "positions"}, {3, "freqs"}, {4, "q_gamma"},
+                                             {5, "k_gamma"}, {10, "q_out", true}, {11, "k_out", true}};
+    check_arguments(a, arguments);
+    const Tensor& q = tensor(a[0], "Q");
+    const Heads hq = heads(q, "Q");
+    const ScalarType type = q.scalar_type();
+    Heads hk = {}, ko = {};
+    Tensor q_out, k_out;
+    if (!none(a[1])) {
+        hk = heads(tensor(a[1], "K"), "K", &type);
+        if (hk.tokens != hq.tokens || hk.dim != hq.dim) value_error("K must have the tokens and the dim of Q");
+    } else if (!none(a[5]) || !none(a[11])) {
+        value_error("k_gamma and k_out need K");
+    }
+    const Turns tu = turns(a[2], a[3], hq.tokens);
+    const Gamma qg = gamma_of(a[4], "q_gamma", type, hq), kg = gamma_of(a[5], "k_gamma", type, hk);
+    const c10::cuda::CUDAGuard guard(q.device());
+    if (!none(a[1])) ko = output(a[11], "k_out", q, hk, type, k_out);
+    const Heads qo = output(a[10], "q_out", q, hq, type, q_out);
+    const w8a8_status s = w8a8_qk_norm_rotary(
+        hq.ptr, hk.ptr, qo.ptr, ko.ptr, dtype_of(type), hq.tokens, hq.heads, hk.heads, hq.dim, tu.rot, hq.token, hq.head,
+        hk.token, hk.head, qo.token, qo.head, ko.token, ko.head, qg.ptr, qg.head, kg.ptr, kg.head,
+        static_cast<float>(number(a[6])), static_cast<w8a8_norm_kind>(integer(a[7])), tu.positions, tu.freqs,
+        static_cast<float>(number(a[9])), static_cast<w8a8_rotary_layout>(integer(a[8])),
+        c10::cuda::getCurrentCUDAStream().stream());
+    if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
+    return Py_BuildValue("(NN)", wrap(q_out), wrap(k_out));
+}
+
+// Q, K, V, positions, freqs, k_cache, v_cache, slots, q_gamma, k_gamma, eps, kind, layout, amplitude, q_out
+PyObject* qk_norm_rotary_append(PyObject* const* a) {
+    static constexpr Argument arguments[] = {{0, "Q"}, {1, "K"}, {2, "V"}, {3, "positions"}, {4, "freqs"},
+                                             {5, "k_cache", true}, {6, "v_cache", true}, {7, "slots"}, {8, "q_gamma"},
+                                             {9, "k_gamma"}, {14, "q_out", true}};
+    check_arguments(a, arguments);
+    const Tensor& q = tensor(a[0], "Q");
+    const Heads hq = heads(q, "Q");
+    const ScalarType type = q.scalar_type();
+    const Tensor &k = tensor(a[1], "K"), &v = tensor(a[2], "V");
+    const Tensor &kc = tensor(a[5], "k_cache"), &vc = tensor(a[6], "v_cache");
+    const Heads hk = heads(k, "K", &type), hv = heads(v, "V", &type);
+    const Cache ck = cache(kc, "k_cache", type, true), cv = cache(vc, "v_cache", type, true);
+    if (hk.tokens != hq.tokens || hk.dim != hq.dim) value_error("K must have the tokens and the dim of Q");
+    if (k.sizes() != v.sizes() || ck.heads != hk.heads || ck.dim != hk.dim || kc.sizes() != vc.sizes())
+        value_error("V must have the shape of K, and both caches its heads and dim");
+    const Turns tu = turns(a[3], a[4], hq.tokens);
+    const auto* slots = indices<int64_t>(a[7], ScalarType::Long, hq.tokens, "slots");
+    const Gamma qg = gamma_of(a[8], "q_gamma", type, hq), kg = gamma_of(a[9], "k_gamma", type, hk);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Tensor q_out;
+    const Heads qo = output(a[14], "q_out", q, hq, type, q_out);
+    const int64_t rows = ck.pages * (kc.dim() == 4 ? ck.page_size : 1);
+    const w8a8_status s = w8a8_qk_norm_rotary_append(
+        hq.ptr, hk.ptr, hv.ptr, qo.ptr, ck.ptr, cv.ptr, dtype_of(type), hq.tokens, hq.heads, hk.heads, hq.dim, tu.rot, rows,
+        ck.page_size, hq.token, hq.head, hk.token, hk.head, hv.token, hv.head, qo.token, qo.head, ck.page, ck.token,
+        ck.head, cv.page, cv.token, cv.head, qg.ptr, qg.head, kg.ptr, kg.head, static_cast<float>(number(a[10])),
+        static_cast<w8a8_norm_kind>(integer(a[11])), tu.positions, slots, tu.freqs, static_cast<float>(number(a[13])),
+        static_cast<w8a8_rotary_layout>(integer(a[12])), c10::cuda::getCurrentCUDAStream().stream());
+    if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
+    return wrap(q_out);
+}
+
+// Caches of one shape, [pages, ...] with dense pages.
+struct Caches {
+    std::vector<void*> base;
+    std::vector<int64_t> stride;
+    int64_t pages = 0, page_bytes = 0;
+    Tensor first;
+};
+Caches caches(PyObject* o) {
+    const bool list = PyList_Check(o);
+    if (!list && !PyTuple_Check(o)) type_error("caches must be a list of tensors");
+    const Py_ssize_t n = list ? PyList_GET_SIZE(o) : PyTuple_GET_SIZE(o);
+    if (n == 0) value_error("caches must hold a tensor at least");
+    Caches r;
+    r.base.reserve(n);
+    r.stride.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const auto name = [&] { return "caches[" + std::to_string(i) + "]"; };
+        PyObject* item = list ? PyList_GET_ITEM(o, i) : PyTuple_GET_ITEM(o, i);
+        if (!THPVariable_Check(item)) type_error(name() + " must be a torch.Tensor");
+        const Tensor& t = THPVariable_Unpack(item);
+        if (t.requires_grad() && c10::GradMode::is_enabled())
+            value_error(name() + " requires a gradient and cannot be written in place: detach it, or call under "
+                        "torch.no_grad()");
+        if (!t.is_cuda()) value_error(name() + " must be a CUDA tensor");
+        if (t.dim() < 2) value_error(name() + " must be [pages, ...]");
+        const int64_t pages = t.size(0);
+        int64_t bytes = t.element_size();
+        for (int64_t d = 1; d < t.dim(); ++d) bytes *= t.size(d);
+        if (i == 0) {
+            r.first = t;
+            r.pages = pages;
+            r.page_bytes = bytes;
+        } else {
+            if (t.device() != r.first.device())
+                value_error(name() + " is on " + t.device().str() + ", caches[0] on " + r.first.device().str());
+            if (pages != r.pages || bytes != r.page_bytes) value_error("caches must have the same pages, of one size");
+        }
+        if (!t.is_contiguous() && pages > 0 && !t.select(0, 0).is_non_overlapping_and_dense())
+            value_error(name() + " must have dense pages");
+        r.base.push_back(t.data_ptr());
+        r.stride.push_back(pages > 1 ? t.stride(0) * t.element_size() : bytes);
+    }
+    return r;
+}
+void bump_caches(PyObject* o) {
+    const bool list = PyList_Check(o);
+    const Py_ssize_t n = list ? PyList_GET_SIZE(o) : PyTuple_GET_SIZE(o);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const Tensor& t = THPVariable_Unpack(list ? PyList_GET_ITEM(o, i) : PyTuple_GET_ITEM(o, i));
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+}
+void same_device(const Caches& c, PyObject* o, const char* name) {
+    if (!THPVariable_Check(o)) return;
+    const Tensor& t = THPVariable_Unpack(o);
+    if (t.is_cuda() && t.device() != c.first.device())
+        value_error(std::string(name) + " is on " + t.device().str() + ", caches[0] on " + c.first.device().str());
+}
+
+// caches, src, dst
+PyObject* copy_pages(PyObject* const* a) {
+    const Caches c = caches(a[0]);
+    same_device(c, a[1], "src");
+    same_device(c, a[2], "dst");
+    const int64_t n = tensor(a[1], "src").numel();
+    const auto* src = indices<int32_t>(a[1], ScalarType::Int, n, "src");
+    const auto* dst = indices<int32_t>(a[2], ScalarType::Int, n, "dst");
+    const c10::cuda::CUDAGuard guard(c.first.device());
+    const w8a8_status s =
+        w8a8_copy_pages(c.base.data(), c.stride.data(), static_cast<int64_t>(c.base.size()), c.pages, c.page_bytes, src,
+                        dst, n, c10::cuda::getCurrentCUDAStream().stream());
+    if (s != W8A8_OK) return status(s);
+    bump_caches(a[0]);
+    Py_RETURN_NONE;
+}
+
+// caches, page_table, k_lens, src, dst, new_pages, page_size
+PyObject* fork_sequences(PyObject* const* a) {
+    static constexpr Argument arguments[] = {{1, "page_table", true}, {2, "k_lens", true}, {3, "src"}, {4, "dst"},
+                                             {5, "new_pages"}};
+    const Caches c = caches(a[0]);
+    for (const Argument& g : arguments) same_device(c, a[g.at], g.name);
+    check_arguments(a, arguments);
+    const Table pt = table(a[1], "page_table");
+    const auto* k_lens = indices<int32_t>(a[2], ScalarType::Int, pt.rows, "k_lens");
+    const int64_t n = tensor(a[3], "src").numel();
+    const auto* src = indices<int32_t>(a[3], ScalarType::Int, n, "src");
+    const auto* dst = indices<int32_t>(a[4], ScalarType::Int, n, "dst");
+    const auto* page = indices<int32_t>(a[5], ScalarType::Int, n, "new_pages");
+    const c10::cuda::CUDAGuard guard(c.first.device());
+    const w8a8_status s = w8a8_fork_sequences(
+        c.base.data(), c.stride.data(), static_cast<int64_t>(c.base.size()), c.pages, c.page_bytes, integer(a[6]), pt.ptr,
+        pt.rows, pt.columns, pt.stride, const_cast<int32_t*>(k_lens), src, dst, page, n,
+        c10::cuda::getCurrentCUDAStream().stream());
+    if (s != W8A8_OK) return status(s);
+    bump_written(a, arguments);
+    bump_caches(a[0]);
+    Py_RETURN_NONE;
 }
 
 // A dense CUDA tensor of the given type and shape; null for None.
@@ -408,7 +673,9 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define W8A8_CALL(name, n) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {W8A8_CALL(attention, 12), W8A8_CALL(rotary, 9), W8A8_CALL(rotary_append, 11),
-                         W8A8_CALL(residual_norm_quant, 16), {nullptr, nullptr, 0, nullptr}};
+                         W8A8_CALL(residual_norm_quant, 16), W8A8_CALL(paged_attention, 12),
+                         W8A8_CALL(qk_norm_rotary, 12), W8A8_CALL(qk_norm_rotary_append, 15), W8A8_CALL(copy_pages, 3),
+                         W8A8_CALL(fork_sequences, 7), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "w8a8_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -23,11 +23,21 @@ struct AttentionArgs {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
     float scale_log2;       // scale * log2(e)
     int causal;
+    // Keys in pages (page_table not nullptr; then cu_k is nullptr): key j of sequence b
+    // is row j % page_size of page page_table[b * table_stride + j / page_size].
+    const int* page_table;   // [batch, max_pages]
+    int64_t table_stride;
+    int64_t k_page, v_page;  // strides of pages
+    int pages, page_size, max_pages;
+    // the sequences that a launch takes have few_rows + 1 to most_rows packed rows
+    int few_rows, most_rows;
+    int expected_rows;       // at most, as the caller says
     // filled in by the launchers
     int* counters;
     float* partial;
     int join_rounds;         // of the split kernel's threads over the rows of an item
     int side_heads;
+    int box;                 // keys of a page that one copy fetches
 };
 size_t attention_workspace_bytes(int num_sms);
 // The workspace's counters (its first attention_counter_bytes) are zero
@@ -46,6 +56,14 @@ cudaError_t launch_attention_prompt(const AttentionArgs& a, int dtype, int num_s
 // boxes of 64 x box_heads x box_rows, 128-byte swizzled; elements outside are 0.
 cudaError_t encode_heads(void* encode_fn, CUtensorMap* map, char name, const void* ptr, int dtype, int rows, int heads,
                          int dim, int64_t token, int64_t head, int box_heads, int box_rows, char* detail, size_t n);
+// Tensor map of pages [pages, page_size, heads, dim], boxes of 64 x 1 x box_rows x 1.
+cudaError_t encode_pages(void* encode_fn, CUtensorMap* map, char name, const void* ptr, int dtype, int pages,
+                         int page_size, int heads, int dim, int64_t page, int64_t token, int64_t head, int box_rows,
+                         char* detail, size_t n);
+// Attention over pages.
+size_t paged_attention_workspace_bytes(int num_sms);
+cudaError_t launch_paged_attention(const AttentionArgs& a, int max_queries, int dtype, int num_sms, void* workspace,
+                                   void* encode_fn, cudaStream_t st, char* detail, size_t n);
 cudaError_t attention_read_device_error(unsigned int* code);
 cudaError_t attention_split_read_device_error(unsigned int* code);
 
@@ -65,6 +83,42 @@ struct RotaryArgs {
     float amplitude;
 };
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, int num_sms, cudaStream_t st);
+
+// Norms of the heads of Q and K before their rotary positions.
+struct HeadNorm {
+    const void* gamma;  // [dim] or [heads, dim], or nullptr: 1
+    int64_t stride;     // 0: one row for all heads
+};
+struct NormRotaryArgs {
+    RotaryArgs r;              // k_out and v_out: caches where slots are given
+    HeadNorm q_norm, k_norm;
+    float eps;
+    int layer;
+    int64_t page_size;         // rows of a page of k_out and v_out, 0: no pages
+    int64_t k_page, v_page;    // strides of pages
+};
+cudaError_t launch_norm_rotary(const NormRotaryArgs& a, int dtype, bool half, int num_sms, cudaStream_t st);
+
+// Pages of several caches of one shape, in bytes.
+struct PageCaches {
+    static constexpr int kMost = 192;  // of a launch: 3 KB of its parameters
+    void* base[kMost];
+    int64_t stride[kMost];  // of pages
+    int64_t page_bytes;
+    int count, pages;
+};
+cudaError_t launch_copy_pages(const PageCaches& c, const int* src, const int* dst, int64_t n, cudaStream_t st);
+// Forks of sequences: rows of a page table, lengths, and the last page of each.
+struct ForkArgs {
+    int* table;  // [rows, max_pages]
+    int64_t table_stride;
+    int* k_lens;  // [rows]
+    const int *src, *dst, *page;  // [n]
+    int64_t n;
+    int rows, max_pages, page_size;
+    int tables;  // write the table and the lengths
+};
+cudaError_t launch_fork_sequences(const PageCaches& c, const ForkArgs& f, cudaStream_t st);
 
 // Branch norm, gate, residual, norm, modulation and quantization of [M, K]
 // rows; every pointer after B but H may be nullptr.

@@ -1,9 +1,11 @@
 """The operators between a transformer layer's W8A8 Linears.
 
 `attention` (packed prompts, and few queries over a cache), `rotary` and
-`rotary_append` (rotary positions, and the cache rows written with them) and
-`residual_norm_quant` (branch norm, gate, residual, next norm, modulation and
-int8 quantization in one pass).  As in the rest of the binding a function
+`rotary_append` (rotary positions, and the cache rows written with them),
+`qk_norm_rotary` and `qk_norm_rotary_append` (the same after a norm of every query
+and key head) and `residual_norm_quant` (branch norm, gate, residual, next norm,
+modulation and int8 quantization in one pass); for caches in pages
+`paged_attention`, `copy_pages` and `fork_sequences`.  As in the rest of the binding a function
 only checks its tensors, allocates outputs and passes pointers, sizes and the
 current stream to the library (include/w8a8.h states the arithmetic); here that
 is done in C++ (csrc/binding.cpp), as it would take longer than the kernels of
@@ -47,8 +49,12 @@ def binding():
 def attention_workspace(device=None):
     """A workspace for `attention`, for one stream at a time (the counters at
     its start are, and stay between calls, zero)."""
+    return _workspace(lib().w8a8_attention_workspace_size(), device)
+
+
+def _workspace(size, device):
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    ws = torch.empty(lib().w8a8_attention_workspace_size(), dtype=torch.uint8, device=device)
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
     ws[:lib().w8a8_attention_workspace_zeroed()].zero_()
     return ws
 
@@ -159,6 +165,94 @@ def rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, layout=HAL
     if type(r) is int:
         _check("w8a8_rotary_append", r)
     return r
+
+
+def qk_norm_rotary(Q, K, positions, freqs, q_gamma=None, k_gamma=None, eps=1e-6, kind=RMS_NORM, layout=HALF,
+                   amplitude=1.0, q_out=None, k_out=None):
+    """`rotary` of Q [T, Hq, D] and K [T, Hk, D] (or None) after a norm of every
+    head: RMSNorm (or LayerNorm without shift, kind=LAYER_NORM) over its D
+    elements, times q_gamma / k_gamma ([D], or [heads, D], of Q's type; None: 1),
+    in binary32 up to one rounding of the result.  Returns (Q', K'), new tensors
+    unless q_out / k_out are given; these may be Q and K themselves."""
+    r = (_binding or binding()).qk_norm_rotary(Q, K, positions, freqs, q_gamma, k_gamma, eps, kind, _layout(layout),
+                                               amplitude, q_out, k_out)
+    if type(r) is int:
+        _check("w8a8_qk_norm_rotary", r)
+    return r
+
+
+def qk_norm_rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, q_gamma=None, k_gamma=None, eps=1e-6,
+                          kind=RMS_NORM, layout=HALF, amplitude=1.0, q_out=None):
+    """`qk_norm_rotary` for tokens that join a cache: K, normed and turned, and V
+    of token t go to row slots[t] (int64 [T]) of k_cache / v_cache: rows
+    [rows, Hk, D], or pages [pages, page_size, Hk, D], where row
+    page * page_size + i is row i of a page.  A slot outside the cache (-1 for a
+    padding token) stores nothing.  Returns the normed and turned Q."""
+    r = (_binding or binding()).qk_norm_rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, q_gamma,
+                                                      k_gamma, eps, kind, _layout(layout), amplitude, q_out)
+    if type(r) is int:
+        _check("w8a8_qk_norm_rotary_append", r)
+    return r
+
+
+def paged_attention_workspace(device=None):
+    """A workspace for `paged_attention`, for one stream at a time."""
+    return _workspace(lib().w8a8_paged_attention_workspace_size(), device)
+
+
+def paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q=None, max_queries=None, causal=True, scale=None,
+                    out=None, lse=False, workspace=None):
+    """`attention` of new tokens over a cache in pages: from one to thousands of
+    them for each sequence, of both kinds in one call.
+
+    Q [Tq, Hq, D] as in `attention`; k_pages, v_pages [pages, page_size, Hk, D]
+    (any strides, the last dimension dense; page_size a multiple of 8).  Key j of
+    sequence b is row j % page_size of page page_table[b, j // page_size]
+    (int32 [B, most pages]; what lies past the last page is not read, an entry
+    outside the cache reads as zeros).  k_lens: int32 [B] keys of each sequence,
+    its new tokens (which are in the cache already) included.  cu_q: int32
+    [B + 1] first rows of the sequences' queries; without it the rows are B equal
+    parts.  max_queries: the most queries of a sequence, where the host knows it;
+    it only spares the kernel that would serve more.  causal, scale, out and lse as
+    in `attention`; rows of no sequence are not written.
+
+    The workspace (`paged_attention_workspace()`) is by default one per
+    stream, kept until the process ends, and one of its own, in the graph's
+    memory, for a captured call."""
+    r = (_binding or binding()).paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q, max_queries, causal,
+                                                scale, out, lse, workspace)
+    if type(r) is int:
+        _check("w8a8_paged_attention", r)
+    return r
+
+
+def copy_pages(caches, src, dst):
+    """Page dst[i] = page src[i] (int32 [n], on the GPU) in every one of `caches`:
+    a list of tensors [pages, ...] with dense pages, such as every layer's k_pages
+    and v_pages.  A pair with an index outside the cache (-1) copies nothing.  No
+    page may be a destination twice, or a destination and a source.
+
+    A cache is compacted by copies of its last pages to free ones before them, and
+    map[page_table] with map = arange(pages), map[src] = dst."""
+    r = (_binding or binding()).copy_pages(caches, src, dst)
+    if type(r) is int:
+        _check("w8a8_copy_pages", r)
+
+
+def fork_sequences(caches, page_table, k_lens, src, dst, new_pages, page_size):
+    """Sequence dst[i] (a row of page_table [rows, most pages] and of k_lens
+    [rows], int32) becomes a second one like src[i] that can go on by itself: it
+    gets its length and its full pages, and page new_pages[i] for what comes next,
+    into which the last page is copied, in every one of `caches` (as in
+    `copy_pages`), where it is only partly filled.  src, dst, new_pages: int32 [n],
+    on the GPU.  Nothing happens where src[i] == dst[i], or where a row or the
+    new page is outside the table or the cache (-1).  A row may be the source of
+    many, but no row a destination twice, or a destination and a source, and no
+    new page used twice or part of a sequence.  Which pages are free, and how many
+    sequences share one, is the caller's to know."""
+    r = (_binding or binding()).fork_sequences(caches, page_table, k_lens, src, dst, new_pages, page_size)
+    if type(r) is int:
+        _check("w8a8_fork_sequences", r)
 
 
 def residual_norm_quant(X, B, gamma=None, beta=None, eps=1e-6, kind=RMS_NORM, alpha=1.0, gate=None, branch_gamma=None,
