@@ -1098,7 +1098,8 @@ w8a8_status w8a8_get_device_error(int* code) {
     }
     cudaError_t (*const readers[])(unsigned int*) = {
         w8a8::gemm_read_device_error,      w8a8::gemm_s8_read_device_error,         w8a8::quant_read_device_error,
-        w8a8::attention_read_device_error, w8a8::attention_split_read_device_error, w8a8::residual_norm_read_device_error};
+        w8a8::attention_read_device_error, w8a8::attention_split_read_device_error, w8a8::residual_norm_read_device_error,
+        w8a8::attention_paged_read_device_error};
     unsigned int v = 0;
     if (w8a8::read_device_errors(readers, &v) != cudaSuccess) return W8A8_ERR_CUDA;
     *code = static_cast<int>(v);

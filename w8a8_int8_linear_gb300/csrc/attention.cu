@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     constexpr int kDT = DP / 8;       // 8-wide output column tiles
     constexpr float kScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;  // of p and O, not of the sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (kPaged) grid_launch_dependents();  // (the kernel of many queries, where both run)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* empty = full + S;
     float* join = reinterpret_cast<float*>(smem + L::kJoin);
@@ -675,14 +676,13 @@ cudaError_t launch_split_typed(const CUtensorMap (&map)[2], const AttentionArgs&
                      : launch_split<__half, 128, kPaged>(map, a, num_sms, st);
 }
 
-// Heads that run side by side: the largest divisor of Hk up to 8.
+}  // namespace
+
 int side_heads(int Hk) {
     for (int h = 8; h > 1; --h)
         if (Hk % h == 0) return h;
     return 1;
 }
-
-}  // namespace
 
 // a counter for each of up to two CTAs per SM
 size_t attention_counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 8 + 255) / 256 * 256; }

@@ -38,6 +38,7 @@ struct AttentionArgs {
     int join_rounds;         // of the split kernel's threads over the rows of an item
     int side_heads;
     int box;                 // keys of a page that one copy fetches
+    void* joins;             // what pieces there are to join, by CTA
 };
 size_t attention_workspace_bytes(int num_sms);
 // The workspace's counters (its first attention_counter_bytes) are zero
@@ -61,11 +62,14 @@ cudaError_t encode_pages(void* encode_fn, CUtensorMap* map, char name, const voi
                          int page_size, int heads, int dim, int64_t page, int64_t token, int64_t head, int box_rows,
                          char* detail, size_t n);
 // Attention over pages.
+// Heads that run side by side: the largest divisor of Hk up to 8.
+int side_heads(int Hk);
 size_t paged_attention_workspace_bytes(int num_sms);
 cudaError_t launch_paged_attention(const AttentionArgs& a, int max_queries, int dtype, int num_sms, void* workspace,
                                    void* encode_fn, cudaStream_t st, char* detail, size_t n);
 cudaError_t attention_read_device_error(unsigned int* code);
 cudaError_t attention_split_read_device_error(unsigned int* code);
+cudaError_t attention_paged_read_device_error(unsigned int* code);
 
 // One [rows, heads, dim] side of the rotary kernel; strides count elements.
 struct Heads {
