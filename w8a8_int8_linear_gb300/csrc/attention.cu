@@ -128,12 +128,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return y;
 }
 
-// a / b for positive a and b, in 32 bits where a allows.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 template <typename T, int DP, int R, int G, bool kPaged>
 __global__ void __launch_bounds__(threads_of(G), 3 - G)
     attention_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -147,7 +141,6 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     constexpr int kDT = DP / 8;       // 8-wide output column tiles
     constexpr float kScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;  // of p and O, not of the sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (kPaged) grid_launch_dependents();  // (the kernel of many queries, where both run)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* empty = full + S;
     float* join = reinterpret_cast<float*>(smem + L::kJoin);
@@ -294,31 +287,22 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
         for (bool more = true; more && ok;) {
             const int t_end = piece_end(), hg = c.item / c.blocks, rb = c.item - hg * c.blocks;
             const int end = seen_end(rb, t_end), hk = hg * p.side_heads + side;
-            // keys in pages: lane i fetches the tile's box i, from the page that it looked up
-            // while the tile before was waited for
-            const auto look_up = [&](int t) {
-                const int key = t * kTile + lane * p.box;
-                return key < min(c.s.m, (t + 1) * kTile) ? page_of(p, c.b, key) : p.pages;
-            };
-            int page = kPaged && c.tile < end ? look_up(c.tile) : 0;
+            Boxes<kTile> boxes;
+            if (kPaged && c.tile < end) boxes.start(p, c.b, c.s.m, c.tile);
             for (int t = c.tile; t < end; ++t) {
-                const int next_page = kPaged && t + 1 < end ? look_up(t + 1) : 0;
+                if (kPaged) boxes.step(p);
                 ok = mbar_wait(&empty[st], ph ^ 1, 50);
                 if (!ok) break;
                 if (kPaged) {
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kStage);
-                    __syncwarp();
-                    if (lane * p.box < kTile) {
-                        const int key = t * kTile + lane * p.box, row = key % p.page_size;
-                        const uint32_t dst = smem_u32(smem) + st * L::kStage + lane * p.box * 128;
+                    if (elect_one_sync()) mbar_arrive_expect_tx(&full[st], L::kStage);
+                    boxes.each([&](int i, int row, int page) {
+                        const uint32_t dst = smem_u32(smem) + st * L::kStage + i * p.box * 128;
 #pragma unroll
                         for (int x = 0; x < DP / 64; ++x) {
                             tma_load_page(dst + x * L::kChunk, &tmK, &full[st], 64 * x, hk, row, page);
                             tma_load_page(dst + L::kKv + x * L::kChunk, &tmV, &full[st], 64 * x, hk, row, page);
                         }
-                    }
-                    __syncwarp();
-                    page = next_page;
+                    });
                 } else if (elect_one_sync()) {
                     mbar_arrive_expect_tx(&full[st], L::kStage);
                     const uint32_t dst = smem_u32(smem) + st * L::kStage;

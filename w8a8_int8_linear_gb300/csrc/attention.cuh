@@ -31,6 +31,12 @@ struct Sequence {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
+// a / b for positive a and b, in 32 bits where a allows.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 template <bool kPaged = false>
 __device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
     Sequence s;
@@ -42,8 +48,6 @@ __device__ __forceinline__ Sequence sequence(const AttentionArgs& p, int b) {
         s.q0 = b * s.n;
     }
     if (kPaged) {
-        const int64_t rows = static_cast<int64_t>(s.n) * p.group;
-        if (rows <= p.few_rows || rows > p.most_rows) s.n = 0;  // another launch's
         s.k0 = 0;
         s.m = clampi(p.k_lens[b], 0, p.max_pages * p.page_size);
         return s;
@@ -69,15 +73,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* tmap,
         : "memory");
 }
 
-// The page of key `key` of sequence b, for a key below its length; one that is not in
-// the cache comes as `pages`, where copies read zeros.
-__device__ __forceinline__ int page_of(const AttentionArgs& p, int b, int key) {
-    const unsigned page = static_cast<unsigned>(
-        __ldg(p.page_table + static_cast<int64_t>(b) * p.table_stride + static_cast<unsigned>(key) / static_cast<unsigned>(p.page_size)));
-    return static_cast<int>(min(page, static_cast<unsigned>(p.pages)));
+// Page `index` of sequence b, for an index of one of its keys; one that is not in the
+// cache comes as `pages`, where copies read zeros.
+__device__ __forceinline__ unsigned entry_of(const AttentionArgs& p, int b, unsigned index) {
+    return static_cast<unsigned>(__ldg(p.page_table + static_cast<int64_t>(b) * p.table_stride + index));
+}
+__device__ __forceinline__ int page_of(const AttentionArgs& p, unsigned entry) {
+    return static_cast<int>(min(entry, static_cast<unsigned>(p.pages)));
 }
 
-// The same from pages: a box of one page.
+// Copy of a box of one page into this CTA's shared memory.
 __device__ __forceinline__ void tma_load_page(uint32_t smem_dst, const void* tmap, uint64_t* bar, int32_t c0,
                                               int32_t head, int32_t row, int32_t page) {
     asm volatile(
@@ -86,6 +91,68 @@ __device__ __forceinline__ void tma_load_page(uint32_t smem_dst, const void* tma
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(head), "r"(row), "r"(page)
         : "memory");
 }
+
+// Where the boxes of a sequence's key tiles (of kTile keys) lie, by a warp: lane i has
+// box i of a tile.  The entry of a box is on its way for a tile's time before it is
+// used, and there are no divisions.
+template <int kTile>
+struct Boxes {
+    int boxes;            // of a tile
+    int key, index, row;  // of this lane's box of the next tile
+    int pages, rest;      // a tile's keys by the page, and what is left of them
+    int m, b;
+    unsigned entry;       // of the next tile's box
+    int page, at_row;     // of the present one's
+
+    __device__ __forceinline__ void look_up(const AttentionArgs& p) {
+        entry = ~0u;  // past the keys: no page
+        if (threadIdx.x % 32 < boxes && key < m) entry = entry_of(p, b, index);
+    }
+    // before key tile `tile` of sequence `seq` with `keys` keys
+    __device__ __forceinline__ void start(const AttentionArgs& p, int seq, int keys, int tile) {
+        boxes = kTile / p.box;
+        b = seq;
+        m = keys;
+        key = tile * kTile + static_cast<int>(threadIdx.x % 32) * p.box;
+        index = static_cast<unsigned>(key) / static_cast<unsigned>(p.page_size);
+        row = key - index * p.page_size;
+        pages = kTile / p.page_size;
+        rest = kTile - pages * p.page_size;
+        look_up(p);
+    }
+    // on to the next tile
+    __device__ __forceinline__ void step(const AttentionArgs& p) {
+        page = page_of(p, entry);
+        at_row = row;
+        key += kTile;
+        row += rest;
+        index += pages;
+        if (row >= p.page_size) {
+            row -= p.page_size;
+            ++index;
+        }
+        look_up(p);
+    }
+    // copy(i, row, page) for every box i, by one thread (the copies of several threads
+    // go one by one, and slowly)
+    template <typename F>
+    __device__ __forceinline__ void each(F copy) const {
+        constexpr int kAtOnce = 4;
+        for (int i0 = 0; i0 < boxes; i0 += kAtOnce) {
+            int pg[kAtOnce], rw[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                pg[i] = __shfl_sync(0xffffffffu, page, i0 + i);
+                rw[i] = __shfl_sync(0xffffffffu, at_row, i0 + i);
+            }
+            if (elect_one_sync()) {
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+                    if (i == 0 || i0 + i < boxes) copy(i0 + i, rw[i], pg[i]);
+            }
+        }
+    }
+};
 
 // 32 lanes x 16 consecutive 32-bit columns from registers.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {

@@ -81,7 +81,8 @@ struct PromptSmem {
     static constexpr int kOut = kPipe + kStages * kTileBytes;  // 32 rows of 64 outputs for each softmax warp
     static constexpr int kOutBytes = 32 * 128;
     static constexpr int kBars = kOut + kSoftmaxWarps * kOutBytes;
-    static constexpr int kTotal = kBars + 768;
+    static constexpr int kHanded = kBars + 768;  // reference and sum of 128 rows
+    static constexpr int kTotal = kHanded + 1024;
     static constexpr int kBuffers = DP == 128 ? 2 : 3;  // of S and P in TMEM
     static constexpr int kOutputs = 128 * kBuffers;     // TMEM column of tile 0's O
 };
@@ -99,17 +100,19 @@ struct Item {
     // first, j0
     int b, j0;
     int slot;           // where its partial result goes; -1: the piece is all there is
+    int last_tile;      // of the whole item
+    int seen;           // keys of the sequence that every row sees
 };
 
-// What the join of an item's pieces needs of it; by CTA, for the item whose first
-// piece is the CTA's last.
+// What the join of an item's pieces needs of it: a seat for each piece, two a CTA
+// (slot 0: the end of an item that an earlier CTA began, or its middle; slot 1: the
+// beginning of one that a later CTA goes on with).
 struct Join {
     int q0, n, m, hk, token0, tiles;
-    int last;           // range of the last piece; -1: nothing to join
+    int first, last;    // ranges of the first and the last piece; last < 0: no piece
 };
-// The partial result of a piece, for each of its two tiles: references of the 128
-// rows, their sums, and the outputs [DP / 4][128 rows][4], so that a warp writes and
-// reads 512 bytes at once with a row per lane.
+// The partial result of a piece, for each of its two tiles: (reference, sum) of the
+// 128 rows, then their outputs [128][DP].
 template <int DP>
 constexpr int kTilePart = kTileRows * (DP + 2);
 
@@ -124,6 +127,8 @@ struct Bars {
     // in the ring, as the cleaners run up to three tiles ahead of the products
     uint64_t v_issued[4], v_clean[4];
     uint64_t item_full[2], item_empty[2], done;
+    // a tile alone: the second half's reference, sum and O are there, and have been read
+    uint64_t handed[4], taken[4];
     uint32_t tmem;
     Item items[2];
 };
@@ -292,15 +297,16 @@ struct Items {
 };
 
 // The pieces of a call over pages, by one warp.  An item (two tiles of rows of a
-// sequence and KV head) has as many key tiles as some of its rows see, and counts
-// kEnds more for its end; all items are laid end to end, sequences outermost, then
-// groups of `side_heads` KV heads (the CTAs side by side take the same range for
-// each of them), then rows, and cut into equal ranges, one per CTA.
+// sequence and KV head, or the last one) has as many key tiles as some of its rows
+// see.  All items are laid end to end, sequences outermost, then groups of
+// `side_heads` KV heads (the CTAs side by side take the same range for each of them),
+// then rows, and cut into equal ranges, one per CTA.  A key tile counts a unit for
+// each tile of rows, and an item's end kEnds.
 struct Pieces {
-    static constexpr int kEnds = 1;
-    int64_t w, w_end, per;
+    static constexpr int kEnds = 3;
+    int64_t w, w_end, per, item_start;
     int b, blocks, groups, hg, block, at;  // at: in the item's part of the line
-    int tiles, line;                       // key tiles of the item, its part of the line
+    int tiles, each, line;                 // the item's key tiles, units of one, its part of the line
     Sequence s;
     int pair_tokens, side, range;
 
@@ -310,18 +316,23 @@ struct Pieces {
     __device__ __forceinline__ int tiles_of(const AttentionArgs& p, const Sequence& q, int i) const {
         return (limit(p, q, min((i + 1) * pair_tokens, q.n) - 1) + kKeyTile - 1) / kKeyTile;
     }
-    __device__ __forceinline__ int line_of(int t) const { return max(t, 1) + kEnds; }
-    __device__ __forceinline__ int blocks_of(const Sequence& q) const { return (q.n + pair_tokens - 1) / pair_tokens; }
-    // the line of one group of heads of a sequence
-    __device__ __forceinline__ int64_t line_of(const AttentionArgs& p, const Sequence& q) const {
-        int64_t sum = 0;
-        const int n = blocks_of(q);
-        for (int i = 0; i < n; ++i) sum += line_of(tiles_of(p, q, i));
-        return sum;
+    __device__ __forceinline__ int units_of(const Sequence& q, int i) const {
+        return i * pair_tokens + pair_tokens / 2 < q.n ? 2 : 1;
     }
+    __device__ __forceinline__ int line_of(const AttentionArgs& p, const Sequence& q, int i) const {
+        return max(tiles_of(p, q, i), 1) * units_of(q, i) + kEnds;
+    }
+    __device__ __forceinline__ int blocks_of(const Sequence& q) const { return (q.n + pair_tokens - 1) / pair_tokens; }
+    // this lane's sequence's line, and inclusive over the lanes
     __device__ __forceinline__ void lines(const AttentionArgs& p, int b0, int64_t& mine, int64_t& incl) const {
         const int lane = threadIdx.x & 31;
-        mine = b0 + lane < p.batch ? groups * line_of(p, sequence<true>(p, b0 + lane)) : 0;
+        mine = 0;
+        if (b0 + lane < p.batch) {
+            const Sequence q = sequence<true>(p, b0 + lane);
+            const int n = blocks_of(q);
+            for (int i = 0; i < n; ++i) mine += line_of(p, q, i);
+        }
+        mine *= groups;
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -331,7 +342,8 @@ struct Pieces {
     }
     __device__ __forceinline__ void item(const AttentionArgs& p) {
         tiles = tiles_of(p, s, block);
-        line = line_of(tiles);
+        each = units_of(s, block);
+        line = max(tiles, 1) * each + kEnds;
     }
 
     // false: nothing for this CTA
@@ -343,11 +355,22 @@ struct Pieces {
         groups = p.Hk / p.side_heads;
         const int ranges = gridDim.x / p.side_heads;
         int64_t mine, incl, total = 0;
-        for (int b0 = (p.batch - 1) / 32 * 32; b0 >= 0; b0 -= 32) {
-            lines(p, b0, mine, incl);
-            total += __shfl_sync(0xffffffffu, incl, 31);
+        if (p.batch == 1) {  // by all lanes
+            const Sequence q = sequence<true>(p, 0);
+            const int n = blocks_of(q);
+            mine = 0;
+            for (int i = lane; i < n; i += 32) mine += line_of(p, q, i);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            mine *= groups;
+            incl = total = mine;
+        } else {
+            for (int b0 = (p.batch - 1) / 32 * 32; b0 >= 0; b0 -= 32) {
+                lines(p, b0, mine, incl);
+                total += __shfl_sync(0xffffffffu, incl, 31);
+            }
         }
-        per = max(static_cast<int64_t>(1 + kEnds), (total + ranges - 1) / ranges);
+        per = max(static_cast<int64_t>(2 + kEnds), quotient(total + ranges - 1, ranges));
         w = per * range;
         w_end = min(total, w + per);
         if (w >= w_end) return false;
@@ -366,11 +389,14 @@ struct Pieces {
         }
         s = sequence<true>(p, b);
         blocks = blocks_of(s);
-        const int64_t of_group = mine / groups;
-        hg = static_cast<int>(left / of_group);
-        left -= hg * of_group;
+        hg = 0;
+        if (groups > 1) {
+            const int64_t of_group = quotient(mine, groups);
+            hg = static_cast<int>(quotient(left, of_group));
+            left -= hg * of_group;
+        }
         for (int i0 = 0;; i0 += 32) {
-            const int one = i0 + lane < blocks ? line_of(tiles_of(p, s, i0 + lane)) : 0;
+            const int one = i0 + lane < blocks ? line_of(p, s, i0 + lane) : 0;
             int sum = one;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -407,14 +433,14 @@ struct Pieces {
         return true;
     }
 
-    // The next piece; any = 0 at the end.  `join` is filled in where it is the first of several.
-    __device__ __forceinline__ Item next(const AttentionArgs& p, Join& join) {
+    // The next piece; any = 0 at the end.
+    __device__ __forceinline__ Item next(const AttentionArgs& p) {
         Item it{};
         while (w < w_end) {
             const int end = static_cast<int>(min(static_cast<int64_t>(line), at + (w_end - w)));
-            const int from = at, most = max(tiles, 1);
-            const int64_t start = w - at;
-            const bool some = from < most;
+            // a key tile belongs to the range that its first unit lies in
+            const int most = max(tiles, 1), from = (at + each - 1) / each, to = min((end + each - 1) / each, most);
+            const bool some = from < to;
             if (some) {
                 it.any = 1;
                 it.q0 = s.q0;
@@ -423,14 +449,14 @@ struct Pieces {
                 it.b = b;
                 it.hk = hg * p.side_heads + side;
                 it.token0 = block * pair_tokens;
-                it.tiles = it.token0 + pair_tokens / 2 < s.n ? 2 : 1;
+                it.tiles = each;
                 it.j0 = from;
-                it.keys = min(end, tiles) - from;
-                it.edge = clampi(limit(p, s, it.token0) / kKeyTile - from, 0, it.keys);
-                const bool whole = from == 0 && end >= most;
-                it.slot = whole ? -1 : 2 * blockIdx.x + (from == 0);
-                if (from == 0 && !whole)
-                    join = {it.q0, it.n, it.m, it.hk, it.token0, it.tiles, static_cast<int>((start + most - 1) / per)};
+                it.keys = min(to, tiles) - from;
+                it.seen = limit(p, s, it.token0);
+                it.edge = clampi(it.seen / kKeyTile - from, 0, it.keys);
+                it.slot = from == 0 && to == most ? -1 : 2 * blockIdx.x + (from == 0);
+                item_start = w - at;
+                it.last_tile = most - 1;
             }
             w += end - at;
             at = end;
@@ -438,6 +464,13 @@ struct Pieces {
             if (some) break;
         }
         return it;
+    }
+
+    // The seat of a piece at its item's join: the ranges in which its first and its
+    // last key tile begin.
+    __device__ __forceinline__ Join seat(const Item& it) const {
+        return {it.q0, it.n, it.m, it.hk, it.token0, it.tiles, static_cast<int>(quotient(item_start, per)),
+                static_cast<int>(quotient(item_start + it.last_tile * it.tiles, per))};
     }
 };
 
@@ -448,11 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     using L = PromptSmem<DP>;
     constexpr int S = L::kStages;
-    if (kPaged) grid_launch_dependents();
+    if (kPaged) grid_launch_dependents();  // the join, which waits for this grid's end
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles start at multiples of 1024
         if (threadIdx.x == 0) record_device_error(1);
-        if (kPaged && threadIdx.x == 0) static_cast<Join*>(p.joins)[blockIdx.x].last = -1;
+        if (kPaged && threadIdx.x < 2) static_cast<Join*>(p.joins)[2 * blockIdx.x + threadIdx.x].last = -1;
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -480,7 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&bars->v_issued[i], 1);
-                mbar_init(&bars->v_clean[i], 2);
+                mbar_init(&bars->v_clean[i], kPaged ? 1 : 2);
+            }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&bars->handed[i], 1);
+                mbar_init(&bars->taken[i], 1);
             }
             mbar_init(&bars->done, 1);
             fence_mbarrier_init();
@@ -489,6 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
         tc_fence_before();
+    }
+    Pieces pieces;
+    bool some = true;
+    Join* joins = static_cast<Join*>(p.joins) + 2 * blockIdx.x;
+    if (kPaged && warp == kSoftmaxWarps + 1) {
+        if (elect_one_sync()) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        if (lane == 0) joins[0].last = joins[1].last = -1;
+        some = pieces.start(p, tile_tokens);
     }
     __syncthreads();
     tc_fence_after();
@@ -504,19 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kPaged ? 80 : 72>();  // (of 168 a thread at launch: 8 warps of 208 and 4 of 80)
         if (warp == kSoftmaxWarps + 1) {
             // ---- items and TMA loads: K_0 Q_0 Q_1 K_1 V_0 ...
-            if (elect_one_sync()) {
+            if (!kPaged && elect_one_sync()) {
                 tma_prefetch_desc(&tmQ);
                 tma_prefetch_desc(&tmK);
                 tma_prefetch_desc(&tmV);
             }
             const uint32_t q_bytes = L::kChunks * tile_tokens * p.group * 128;
             Items items;
-            Pieces pieces;
-            Join join;
-            join.last = -1;
-            bool some = true;
-            if (kPaged) some = pieces.start(p, tile_tokens);
-            else items.start(p, tile_tokens, kKeyTile);
+            if (!kPaged) items.start(p, tile_tokens, kKeyTile);
             int index = blockIdx.x, edges = 0;
             int q_ph[2] = {1, 1};  // a fresh barrier lets the first wait through
             Ring<S> r;
@@ -525,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int at = 0; ok; ++at) {
                 Item it{};
                 if (!kPaged) it = items.find(p, index);
-                else if (some) it = pieces.next(p, join);
+                else if (some) it = pieces.next(p);
                 if (!mbar_wait(&bars->item_empty[at & 1], ((at >> 1) & 1) ^ 1, 60)) {
                     it.any = 0;
                     ok = false;
@@ -537,36 +581,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!it.any) break;
                 if (!kPaged && lane == 0) index = atomicAdd(p.counters, 1);
                 const int jmax = it.keys;
-                // keys in pages: lane i fetches box i of a tile, from the page that it looked up
-                // a key tile before
-                const auto look_up = [&](int j) {
-                    const int key = (it.j0 + j) * kKeyTile + lane * p.box;
-                    return lane * p.box < kKeyTile && key < it.m ? page_of(p, it.b, key) : p.pages;
-                };
-                int page_even = 0, page_odd = 0, page_next = kPaged && jmax > 0 ? look_up(0) : 0;
+                Boxes<kKeyTile> boxes;
+                if (kPaged && jmax > 0) boxes.start(p, it.b, it.m, it.j0);
                 for (int i = 0; i < 2 * jmax; ++i) {
                     const int j = load_tile(i, jmax);
                     const bool is_v = load_is_v(i, jmax);
+                    if (kPaged && is_v) {  // another warp's
+                        r.next();
+                        continue;
+                    }
                     ok = mbar_wait(&bars->kv_empty[r.st], r.ph, 61);
                     if (!ok) break;
                     const void* map = is_v ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
                     if (kPaged) {
-                        if (!is_v) {
-                            (j & 1 ? page_odd : page_even) = page_next;  // until V of this tile
-                            if (j + 1 < jmax) page_next = look_up(j + 1);
-                        }
-                        const int page = j & 1 ? page_odd : page_even;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
-                        __syncwarp();
-                        if (lane * p.box < kKeyTile) {
-                            const int row = ((it.j0 + j) * kKeyTile + lane * p.box) % p.page_size;
-                            const uint32_t dst = pipe + r.st * L::kTileBytes + lane * p.box * 128;
+                        boxes.step(p);
+                        if (elect_one_sync()) mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
+                        boxes.each([&](int x, int row, int page) {
+                            const uint32_t dst = pipe + r.st * L::kTileBytes + x * p.box * 128;
 #pragma unroll
                             for (int c = 0; c < L::kChunks; ++c)
-                                tma_load_page(dst + c * kChunkBytes, map, &bars->kv_full[r.st], 64 * c, it.hk, row, page);
-                        }
-                        if (lane == 0 && is_v && j >= it.edge) mbar_arrive(&bars->v_issued[(edges + j - it.edge) & 3]);
-                        __syncwarp();
+                                tma_load_page(dst + c * kChunkBytes, &tmK, &bars->kv_full[r.st], 64 * c, it.hk, row, page);
+                        });
                     } else if (elect_one_sync()) {
                         mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
 #pragma unroll
@@ -595,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 edges += max(0, jmax - it.edge);
+                if (kPaged && lane == 0 && it.slot >= 0) joins[it.slot & 1] = pieces.seat(it);
                 if (!kPaged) index = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, index, 0);
             }
             // nothing is in flight into this CTA's shared memory when it ends
@@ -605,9 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r.next();
             }
             for (int t = 0; t < 2; ++t) mbar_wait(&bars->q_full[t], q_ph[t], 62);
-            if (kPaged) {
-                if (lane == 0) static_cast<Join*>(p.joins)[blockIdx.x] = join;
-            } else if (lane == 0) {  // the last CTA to run out of items leaves the counters at zero
+            if (!kPaged && lane == 0) {  // the last CTA to run out of items leaves the counters at zero
                 __threadfence();
                 if (atomicAdd(p.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
                     p.counters[0] = 0;
@@ -684,6 +718,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                         rv.next(load_of_v(j + 1, J) - load_of_v(j, J));
                     }
                 };
+                // a tile alone: its key tiles go to O of tile 0 and of tile 1 in turn
+                auto run_alone = [&](int J, int edge) {
+                    Ring<S> rk = r, rv = r;
+                    rv.next(load_of_v(0, J));
+                    auto scores = [&](int j, int to) {
+                        const uint32_t b = (kv_low + rk.st * kTileLow) | kDescKMajor;
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k) {
+                            const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4;
+                            mma_scores(tmem + 128 * to, q_low + off, b + off, prompt_idesc<T>(kKeyTile, false), k > 0);
+                        }
+                        mma_commit(&bars->s_full[j & 1][own[j & 1] & 3]);
+                        ++own[j & 1];
+                        if (j + 1 == J) mma_commit(&bars->q_empty[0]);
+                        mma_commit(&bars->kv_empty[rk.st]);
+                        rk.next(j == 0 ? 1 : 2);
+                    };
+                    for (int j = 0; j < NB && j < J; ++j) {
+                        if (!(ok = mbar_wait(&bars->kv_full[rk.st], rk.ph, 64))) return;
+                        if (j == 0 && !(ok = mbar_wait(&bars->q_full[0], q_ph & 1, 65))) return;
+                        tc_fence_after();
+                        const int to = buf + j;
+                        scores(j, to >= NB ? to - NB : to);
+                    }
+                    q_ph ^= 1;
+                    for (int j = 0; j < J; ++j) {
+                        if (!(ok = mbar_wait(&bars->kv_full[rv.st], rv.ph, 66))) return;
+                        if (j >= edge) {
+                            if (!(ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67))) return;
+                            ++edges;
+                        }
+                        const uint32_t v_low = (kv_low + rv.st * kTileLow) | kDescMnMajor;
+                        const int t = j & 1;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (!(ok = mbar_wait(&bars->p_full[buf][half], (p_ph >> buf) & 1, 69))) return;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                mma_output(tmem + L::kOutputs + t * DP, tmem + 128 * buf + 8 * k,
+                                           v_low + k * (2048 >> 4), prompt_idesc<T>(DP, true), j > 1 || k > 0);
+                        }
+                        mma_commit(&bars->pv_done[t][pv_own[t] & 3]);
+                        ++pv_own[t];
+                        mma_commit(&bars->kv_empty[rv.st]);
+                        rv.next(load_of_v(j + 1, J) - load_of_v(j, J));
+                        if (j + NB < J) {
+                            if (!(ok = mbar_wait(&bars->kv_full[rk.st], rk.ph, 68))) return;
+                            tc_fence_after();
+                            scores(j + NB, buf);
+                        }
+                        p_ph ^= 1 << buf;
+                        if (++buf == NB) buf = 0;
+                    }
+                };
                 for (int at = 0; ok; ++at) {
                     if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 63)) break;
                     const volatile Item& it = bars->items[at & 1];
@@ -692,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars->item_empty[at & 1]);
                     if (J == 0) continue;
                     if (two) run(std::integral_constant<int, 2>{}, J, edge);
+                    else if (kPaged) run_alone(J, edge);
                     else run(std::integral_constant<int, 1>{}, J, edge);
                     r.skip(2 * J);
                 }
@@ -700,9 +790,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&bars->done, 0, 70);
             }
             __syncwarp();
+        } else if (kPaged && warp == kSoftmaxWarps + 2) {
+            // ---- V from pages (the copies of one warp alone would bound short tiles)
+            Ring<S> r;
+            r.ph = 1;
+            int edges = 0;
+            bool ok = true;
+            for (int at = 0; ok; ++at) {
+                if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 81)) break;
+                const volatile Item& it = bars->items[at & 1];
+                if (!it.any) break;
+                const int jmax = it.keys, hk = it.hk, edge = it.edge;
+                Boxes<kKeyTile> boxes;
+                if (jmax > 0) boxes.start(p, it.b, it.m, it.j0);
+                leave_item(at);
+                for (int i = 0; i < 2 * jmax; ++i, r.next()) {
+                    if (!load_is_v(i, jmax)) continue;
+                    ok = mbar_wait(&bars->kv_empty[r.st], r.ph, 82);
+                    if (!ok) break;
+                    boxes.step(p);
+                    if (elect_one_sync()) mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
+                    boxes.each([&](int x, int row, int page) {
+                        const uint32_t dst = pipe + r.st * L::kTileBytes + x * p.box * 128;
+#pragma unroll
+                        for (int c = 0; c < L::kChunks; ++c)
+                            tma_load_page(dst + c * kChunkBytes, &tmV, &bars->kv_full[r.st], 64 * c, hk, row, page);
+                    });
+                    const int j = load_tile(i, jmax);
+                    if (j >= edge && elect_one_sync()) mbar_arrive(&bars->v_issued[(edges + j - edge) & 3]);
+                }
+                edges += max(0, jmax - edge);
+            }
+            for (int i = 0; i < S; ++i) {  // nothing is in flight when the CTA ends
+                mbar_wait(&bars->kv_full[r.st], r.ph, 82);
+                r.next();
+            }
         } else {
             // ---- V cleaners: key tiles from `edge` on
-            const int me = threadIdx.x - 32 * (kSoftmaxWarps + 2);  // 0..63
+            constexpr int kCleaners = kPaged ? 32 : 64;
+            const int me = threadIdx.x - 32 * (kSoftmaxWarps + 4) + kCleaners;  // 0 .. kCleaners - 1
             int ld = 0, edges = 0;
             bool ok = true;
             for (int at = 0; ok; ++at) {
@@ -717,14 +843,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t v = pipe + (lv % S) * L::kTileBytes;
                     constexpr int kAtOnce = 8;  // loads in flight: one by one they would bound an item's end
-                    static_assert(L::kTileBytes % (16 * 64 * kAtOnce) == 0, "whole rounds");
-                    for (int c0 = me; c0 < L::kTileBytes / 16; c0 += 64 * kAtOnce) {
+                    static_assert(L::kTileBytes % (16 * kCleaners * kAtOnce) == 0, "whole rounds");
+                    for (int c0 = me; c0 < L::kTileBytes / 16; c0 += kCleaners * kAtOnce) {
+                        // 32 keys at a time, from those on that some row does not see
+                        static_assert(!kPaged || kCleaners * kAtOnce == 32 * 8, "32 keys");
+                        if (kPaged && (it.j0 + j) * kKeyTile + ((c0 - me) / 8 & 127) + 32 <= it.seen) continue;
                         uint4 w[kAtOnce];
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i)
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                                         : "r"(v + 16 * (c0 + 64 * i)));
+                                         : "r"(v + 16 * (c0 + kCleaners * i)));
                         bool some = false;
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i) some |= any_non_finite<T>(w[i]);
@@ -732,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i) {
                             if (!any_non_finite<T>(w[i])) continue;
-                            const int c = c0 + 64 * i;
+                            const int c = c0 + kCleaners * i;
                             constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
                             uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
@@ -766,16 +895,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t to = tmem + lanes + L::kOutputs + t * DP;
         const float c = p.scale_log2;
         const uint64_t c2 = f2_pack(c, c);
+        int alones = 0;          // tiles alone so far
         int steps = 0, own = 0;  // steps of both tiles before this item (mod the buffers), of this tile
         bool ok = true;
         for (int at = 0; ok; ++at) {
             if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 74)) break;
             const volatile Item& it = bars->items[at & 1];
             if (!it.any) break;
+            // a tile alone: both groups' rows are its rows, and the key tiles theirs in turn
+            const int both = it.tiles;
+            const bool alone = kPaged && both == 1;
+            const int j_first = alone ? t : 0, j_step = alone ? 2 : 1;
+            const int my_token = alone ? row / p.group : row_token;
             int lim, warp_lim, sees;  // limits from the first key of the item
             {
-                const int n = it.n, m = it.m, token = it.token0 + row_token;
-                const bool valid = used && t < it.tiles && token < n;
+                const int n = it.n, m = it.m, token = it.token0 + my_token;
+                const bool valid = used && (alone || t < both) && token < n;
                 lim = valid ? (p.causal ? clampi(token + m - n + 1, 0, m) : m) : 0;
                 warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : m);
                 sees = lim;
@@ -784,12 +919,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     warp_lim -= it.j0 * kKeyTile;
                 }
             }
-            const int both = it.tiles, tiles = t < both ? it.keys : 0;
+            const int tiles = alone || t < both ? it.keys : 0;
             float ref = -INFINITY;
             auto base_of = [](float r) { return r == -INFINITY ? 0.0f : kShift<T> - r; };
             uint64_t sum2 = f2_pack(0.0f, 0.0f);
-            for (int j = 0; j < tiles; ++j, ++own) {
-                const int buf = (steps + j * both + t) % L::kBuffers;
+            for (int j = j_first; j < tiles; j += j_step, ++own) {
+                const int buf = (steps + (alone ? j : j * both + t)) % L::kBuffers;
                 const uint32_t ts = tmem + lanes + 128 * buf;
                 ok = mbar_wait(&bars->s_full[t][own & 3], (own >> 2) & 1, 75);
                 if (!ok) break;
@@ -816,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i)
                         m[i] = max3(m[i], __uint_as_float(v[i][k]), __uint_as_float(v[i][k + 1]));
                 const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-                if (j == 0) {
+                if (j == j_first) {
                     ref = top;
                 } else {
                     const bool moves = top > ref + kSlack;  // also from -inf
@@ -871,7 +1006,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- O / sum to memory
             float l0, l1;
             f2_unpack(sum2, l0, l1);
-            const float l = l0 + l1;
+            float l = l0 + l1;
+            float f0 = 1.0f, f1 = 0.0f;  // weights of this group's O and the other's, of a tile alone
+            if (alone) {
+                float2* row_of = reinterpret_cast<float2*>(smem + L::kHanded) + row;
+                if (t == 1) {
+                    if (tiles > 1) ok = ok && mbar_wait(&bars->pv_done[1][(own - 1) & 3], ((own - 1) >> 2) & 1, 78);
+                    if (!ok) break;
+                    *row_of = make_float2(ref, l);
+                    leave_item(at);
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(&bars->handed[wq]);
+                    ok = mbar_wait(&bars->taken[wq], alones & 1, 79);
+                    ++alones;
+                    continue;
+                }
+                ok = ok && mbar_wait(&bars->handed[wq], alones & 1, 80);
+                if (!ok) break;
+                ++alones;
+                const float2 other = *row_of;
+                const float to_ref = fmaxf(ref, other.x);
+                f0 = ref == to_ref ? 1.0f : exp2_approx(ref - to_ref);
+                f1 = other.x == to_ref ? 1.0f : exp2_approx(other.x - to_ref);
+                ref = to_ref;
+                l = l * f0 + other.y * f1;
+            }
             const float inv = sees > 0 ? __frcp_rn(l) : 0.0f;
             // where the rows go: through shared memory, so that eight lanes write 128
             // bytes of a row, this lane 16 bytes of rows sub, sub + 4, ...
@@ -900,12 +1059,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tiles > 0) {
                         tmem_ld_32x32b_x32(to + 64 * i + 32 * q, o);
                         tmem_wait_ld_regs32(o);
+                        if (alone && tiles > 1) {
+                            uint32_t o1[32];
+                            tmem_ld_32x32b_x32(to + DP + 64 * i + 32 * q, o1);
+                            tmem_wait_ld_regs32(o1);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(o1[x]) * f1);
+                        }
+                    }
+                    if (alone && 64 * i + 32 * q + 32 == DP) {  // O of the other group has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->taken[wq]);
                     }
                     if (bad) {
                         for (int key = edge * kKeyTile; key < seen_end; ++key) {
                             int64_t at_row = static_cast<int64_t>(k0 + key) * p.v_token;
                             if (kPaged) {
-                                const int page = page_of(p, b, first + key);
+                                const int page = page_of(
+                                    p, entry_of(p, b, static_cast<unsigned>(first + key) / static_cast<unsigned>(p.page_size)));
                                 if (page == p.pages) continue;  // zeros
                                 at_row = page * p.v_page + (first + key) % p.page_size * p.v_token;
                             }
@@ -919,19 +1092,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (kPaged && slot >= 0) {  // a piece: its own reference, sum and output, for the join
-                        float* part = p.partial + (2 * static_cast<int64_t>(slot) + t) * kTilePart<DP>;
-                        if (valid) {
+                    if (kPaged && slot >= 0) {  // a piece: for the join, 32 columns at a time
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                *reinterpret_cast<uint4*>(part + 2 * kTileRows + ((16 * i + 8 * q + x) * kTileRows + row) * 4) =
-                                    tiles > 0 ? make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3])
-                                              : make_uint4(0, 0, 0, 0);
-                            if (i == 0 && q == 0) {
-                                part[row] = ref;
-                                part[kTileRows + row] = l;
-                            }
-                        }
+                        for (int x = 0; x < 8; ++x)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             stage + lane * 128 + ((x ^ (lane & 7)) << 4)),
+                                         "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+                                         : "memory");
+                        __syncwarp();
+                        uint4 w[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
+                                         : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
+                        float* part = p.partial + (2 * static_cast<int64_t>(slot) + t) * kTilePart<DP>;
+                        if (i == 0 && q == 0 && valid) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(ref, l);
+                        part += 2 * kTileRows + (32 * wq + sub) * DP + 64 * i + 32 * q + 4 * ch;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (valid_rows >> (4 * x) & 1) *reinterpret_cast<uint4*>(part + 4 * x * DP) = w[x];
+                        __syncwarp();
                         continue;
                     }
 #pragma unroll
@@ -974,8 +1155,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    // this grid is not complete before the one that it was launched beside
-    if (kPaged) grid_dependency_wait();
 }
 
 }  // namespace

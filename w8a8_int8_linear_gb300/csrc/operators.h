@@ -29,9 +29,7 @@ struct AttentionArgs {
     int64_t table_stride;
     int64_t k_page, v_page;  // strides of pages
     int pages, page_size, max_pages;
-    // the sequences that a launch takes have few_rows + 1 to most_rows packed rows
-    int few_rows, most_rows;
-    int expected_rows;       // at most, as the caller says
+    int expected_rows;       // packed rows of a sequence at most, as the caller says
     // filled in by the launchers
     int* counters;
     float* partial;
