@@ -24,98 +24,66 @@ constexpr int kFewRows = 16;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinParts = 8;  // blocks of a seat
 
-// Rows row, row + step, ... below `end` of an item, kRows of them and kPieces pieces on
-// their way at once; DP / 4 lanes to a row, this one's columns 4 lane, ... .
-template <typename T, int DP, int kRows, int kPieces>
-__device__ __forceinline__ void join_rows(const AttentionArgs& p, const Join& it, int side, int row, int end, int step,
-                                          int lane) {
-    const auto weight = [](float m, float to) { return m == to ? 1.0f : exp2_approx(m - to); };
-    for (; row < end; row += kRows * step) {
-        float top[kRows], l[kRows];
-        float4 o[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            top[r] = -INFINITY;
-            l[r] = 0.0f;
-            o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-#pragma unroll 1
-        for (int x0 = it.first; x0 <= it.last; x0 += kPieces) {
-            float2 stats[kPieces][kRows];
-            float4 v[kPieces][kRows];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                // the first piece is in its CTA's slot 1, the others in slot 0
-                const int64_t slot = 2 * (static_cast<int64_t>(x0 + i) * p.side_heads + side) + (x0 + i == it.first);
-                const float* src = p.partial + 2 * slot * kTilePart<DP>;
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const int at = row + r * step, t = at / kTileRows, in_tile = at % kTileRows;
-                    stats[i][r] = make_float2(-INFINITY, 0.0f);
-                    v[i][r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (x0 + i > it.last || at >= end) continue;
-                    const float* of_tile = src + t * kTilePart<DP>;
-                    stats[i][r] = __ldcg(reinterpret_cast<const float2*>(of_tile) + in_tile);
-                    v[i][r] = __ldcg(reinterpret_cast<const float4*>(of_tile + 2 * kTileRows + in_tile * DP) + lane);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float to = top[r];
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) to = fmaxf(to, stats[i][r].x);
-                const float f = weight(top[r], to);
-                top[r] = to;
-                l[r] *= f;
-                o[r] = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const float w = weight(stats[i][r].x, to);
-                    const float4 u = v[i][r];
-                    l[r] += stats[i][r].y * w;
-                    o[r] = make_float4(o[r].x + u.x * w, o[r].y + u.y * w, o[r].z + u.z * w, o[r].w + u.w * w);
-                }
-            }
-        }
-        const int tile_tokens = kTileRows / p.group;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int at = row + r * step, in_tile = at % kTileRows;
-            const int token = it.token0 + at / kTileRows * tile_tokens + in_tile / p.group;
-            if (at >= end || in_tile >= tile_tokens * p.group || token >= it.n) continue;
-            const int head = it.hk * p.group + in_tile % p.group;
-            const bool sees = !p.causal || token + it.m - it.n >= 0;  // (a joined item has keys)
-            const float inv = sees ? __frcp_rn(l[r]) : 0.0f;
-            if (4 * lane < p.D)
-                *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + static_cast<int64_t>(it.q0 + token) * p.o_token +
-                                          static_cast<int64_t>(head) * p.o_head + 4 * lane) =
-                    sees ? make_uint2(Pair16<T>::pack(o[r].x * inv, o[r].y * inv),
-                                      Pair16<T>::pack(o[r].z * inv, o[r].w * inv))
-                         : make_uint2(0, 0);
-            if (p.lse && lane == 0)
-                p.lse[static_cast<int64_t>(it.q0 + token) * p.Hq + head] =
-                    sees ? (log2f(l[r]) + (top[r] == -INFINITY ? 0.0f : top[r] - kShift<T>)) * kLn2 : -INFINITY;
-        }
-    }
-}
-
 // The pieces of an item share its join: its rows are dealt out over the blocks of
-// their seats, so that every block reads the same bytes however many pieces an item has.
+// their seats, so that every block reads the same bytes however many pieces an item
+// has.  DP / 4 lanes to a row, four columns each.  The code is kept short: it is
+// fetched from DRAM every time, as keys have driven it out of L2, and written out for
+// few and many pieces (4 KB more) it took 3 to 5 us longer.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kJoinThreads, 6) join_kernel(const AttentionArgs p) {
-    const int seat = blockIdx.x / kJoinParts, part = blockIdx.x % kJoinParts;
-    const int cta = seat >> 1, side = cta % p.side_heads;
-    constexpr int kLanes = DP / 4, kAtOnce = kJoinThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
+__global__ void __launch_bounds__(kJoinThreads, 8) join_kernel(const AttentionArgs p) {
+    constexpr int kLanes = DP / 4, kAtOnce = 4;  // pieces on their way
     grid_dependency_wait();
+    const int seat = blockIdx.x / kJoinParts, cta = seat >> 1;
     const Join it = static_cast<const Join*>(p.joins)[seat];
     if (it.last < 0) return;
-    const int pieces = it.last - it.first + 1, shares = pieces * kJoinParts;
-    const int share = (cta / p.side_heads - it.first) * kJoinParts + part, rows = it.tiles * kTileRows;
-    const int first = rows * share / shares + threadIdx.x / kLanes, end = rows * (share + 1) / shares;
-    if (pieces <= 2) join_rows<T, DP, 4, 2>(p, it, side, first, end, kAtOnce, lane);
-    else if (pieces <= 4) join_rows<T, DP, 2, 4>(p, it, side, first, end, kAtOnce, lane);
-    else join_rows<T, DP, 1, 8>(p, it, side, first, end, kAtOnce, lane);
+    const int side = cta % p.side_heads, pieces = it.last - it.first + 1, shares = pieces * kJoinParts;
+    const int share = (cta / p.side_heads - it.first) * kJoinParts + blockIdx.x % kJoinParts;
+    const int rows = it.tiles * kTileRows, end = rows * (share + 1) / shares, lane = threadIdx.x % kLanes;
+    const int tile_tokens = kTileRows / p.group;
+    // the first piece is in its CTA's slot 1, the others in slot 0
+    const int64_t step = static_cast<int64_t>(4 * p.side_heads) * kTilePart<DP>;
+    const float* from = p.partial + it.first * step + 4 * side * kTilePart<DP>;
+#pragma unroll 1
+    for (int row = rows * share / shares + threadIdx.x / kLanes; row < end; row += kJoinThreads / kLanes) {
+        const int t = row / kTileRows, r = row % kTileRows, token = it.token0 + t * tile_tokens + r / p.group;
+        if (r >= tile_tokens * p.group || token >= it.n) continue;
+        const float* src = from + t * kTilePart<DP>;
+        float top = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int x0 = 0; x0 < pieces; x0 += kAtOnce, src += kAtOnce * step) {
+            float2 stats[kAtOnce];
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float* part = src + i * step + (x0 + i == 0 ? 2 * kTilePart<DP> : 0);
+                stats[i] = make_float2(-INFINITY, 0.0f);
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x0 + i < pieces) {
+                    stats[i] = __ldcg(reinterpret_cast<const float2*>(part) + r);
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(part + 2 * kTileRows + r * DP) + lane);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float to = fmaxf(top, stats[i].x);
+                const float f = top == to ? 1.0f : exp2_approx(top - to), w = stats[i].x == to ? 1.0f : exp2_approx(stats[i].x - to);
+                top = to;
+                l = l * f + stats[i].y * w;
+                o = make_float4(o.x * f + v[i].x * w, o.y * f + v[i].y * w, o.z * f + v[i].z * w, o.w * f + v[i].w * w);
+            }
+        }
+        const bool sees = !p.causal || token + it.m - it.n >= 0;  // (a joined item has keys)
+        const float inv = sees ? __frcp_rn(l) : 0.0f;
+        const int head = it.hk * p.group + r % p.group;
+        const int64_t at = it.q0 + token;
+        if (4 * lane < p.D)
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * p.o_token + head * p.o_head + 4 * lane) =
+                sees ? make_uint2(Pair16<T>::pack(o.x * inv, o.y * inv), Pair16<T>::pack(o.z * inv, o.w * inv))
+                     : make_uint2(0, 0);
+        if (p.lse && lane == 0)
+            p.lse[at * p.Hq + head] = sees ? (log2f(l) + (top == -INFINITY ? 0.0f : top - kShift<T>)) * kLn2 : -INFINITY;
+    }
 }
 
 template <typename T, int DP>

@@ -303,7 +303,7 @@ struct Items {
 // then rows, and cut into equal ranges, one per CTA.  A key tile counts a unit for
 // each tile of rows, and an item's end kEnds.
 struct Pieces {
-    static constexpr int kEnds = 3;
+    static constexpr int kEnds = 6;
     int64_t w, w_end, per, item_start;
     int b, blocks, groups, hg, block, at;  // at: in the item's part of the line
     int tiles, each, line;                 // the item's key tiles, units of one, its part of the line
@@ -1040,109 +1040,152 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int seen_end = kPaged ? min(lim, it.keys * kKeyTile) : lim;
             const int head = hk * p.group + row_head;
             const int sub = lane >> 3, ch = lane & 7;
-            const int64_t mine = static_cast<int64_t>(q0 + token) * p.o_token + static_cast<int64_t>(head) * p.o_head;
             const uint32_t valid_rows = __ballot_sync(0xffffffffu, valid) >> sub;
-            int64_t to_row[8];
+            int64_t mine = static_cast<int64_t>(q0 + token) * p.o_token + static_cast<int64_t>(head) * p.o_head;
+            int64_t to_row[8];  // elements, or over pages an address
+            float* part = nullptr;
+            if constexpr (kPaged) {
+                part = p.partial + (2 * static_cast<int64_t>(slot) + t) * kTilePart<DP>;
+                mine = reinterpret_cast<int64_t>(slot >= 0 ? static_cast<void*>(part + 2 * kTileRows + row * DP)
+                                                           : static_cast<void*>(static_cast<T*>(p.o) + mine));
+            }
 #pragma unroll
-            for (int x = 0; x < 8; ++x) to_row[x] = __shfl_sync(0xffffffffu, mine, 4 * x + sub) + 8 * ch;
+            for (int x = 0; x < 8; ++x) to_row[x] = __shfl_sync(0xffffffffu, mine, 4 * x + sub) + (kPaged ? 0 : 8 * ch);
             if (tiles > 0) ok = ok && mbar_wait(&bars->pv_done[t][(own - 1) & 3], ((own - 1) >> 2) & 1, 76);
             if (!ok) break;
             tc_fence_after();
             const int bad = tiles > 0 ? it.bad : 0;
             leave_item(at);
             const uint32_t stage = smem_u32(smem) + L::kOut + warp * L::kOutBytes;
+            if constexpr (kPaged) {
+                // A whole item's rows in the type, or a piece's in binary32 for the join, 32
+                // columns at a time in one loop: an item's end is run seldom, and fetching
+                // its code takes as long as running it (6 us for the first end on an SM
+                // when the loop was written out for both).
+                const float scale = slot >= 0 ? 1.0f : inv;
 #pragma unroll 1
-            for (int i = 0; i < DP / 64; ++i) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int c = 0; c < DP / 32; ++c) {
                     uint32_t o[32];
                     if (tiles > 0) {
-                        tmem_ld_32x32b_x32(to + 64 * i + 32 * q, o);
+                        tmem_ld_32x32b_x32(to + 32 * c, o);
                         tmem_wait_ld_regs32(o);
                         if (alone && tiles > 1) {
                             uint32_t o1[32];
-                            tmem_ld_32x32b_x32(to + DP + 64 * i + 32 * q, o1);
+                            tmem_ld_32x32b_x32(to + DP + 32 * c, o1);
                             tmem_wait_ld_regs32(o1);
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
                                 o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(o1[x]) * f1);
                         }
                     }
-                    if (alone && 64 * i + 32 * q + 32 == DP) {  // O of the other group has been read
+                    if (alone && 32 * c + 32 == DP) {  // O of the other group has been read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars->taken[wq]);
                     }
-                    if (bad) {
-                        for (int key = edge * kKeyTile; key < seen_end; ++key) {
-                            int64_t at_row = static_cast<int64_t>(k0 + key) * p.v_token;
-                            if (kPaged) {
-                                const int page = page_of(
-                                    p, entry_of(p, b, static_cast<unsigned>(first + key) / static_cast<unsigned>(p.page_size)));
-                                if (page == p.pages) continue;  // zeros
-                                at_row = page * p.v_page + (first + key) % p.page_size * p.v_token;
-                            }
-                            const T* src = static_cast<const T*>(p.v) + at_row + static_cast<int64_t>(hk) * p.v_head +
-                                           64 * i + 32 * q;
+                    const bool some = tiles > 0 && (sees > 0 || slot >= 0);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                if (64 * i + 32 * q + x >= p.D) continue;
+                    for (int x = 0; x < 8; ++x) {
+                        float f[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) f[y] = some ? __uint_as_float(o[4 * x + y]) * scale : 0.0f;
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         stage + lane * 128 + ((x ^ (lane & 7)) << 4)),
+                                     "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3])
+                                     : "memory");
+                    }
+                    if (bad) {  // the non-finite values that this row sees, in its places
+#pragma unroll 1
+                        for (int key = edge * kKeyTile; key < seen_end; ++key) {
+                            const unsigned at_key = first + key, size = p.page_size;
+                            const int page = page_of(p, entry_of(p, b, at_key / size));
+                            if (page == p.pages) continue;  // zeros
+                            const T* src = static_cast<const T*>(p.v) + page * p.v_page + at_key % size * p.v_token +
+                                           hk * p.v_head + 32 * c;
+#pragma unroll 1
+                            for (int x = 0; x < 32 && 32 * c + x < p.D; ++x) {
                                 const float val = static_cast<float>(src[x]);
-                                if (!isfinite(val)) o[x] = __float_as_uint(__uint_as_float(o[x]) + val);
+                                if (isfinite(val)) continue;
+                                const uint32_t place = stage + lane * 128 + (((x >> 2) ^ (lane & 7)) << 4) + 4 * (x & 3);
+                                float f;
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(place) : "memory");
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(place), "f"(f + val) : "memory");
                             }
                         }
                     }
-                    if (kPaged && slot >= 0) {  // a piece: for the join, 32 columns at a time
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             stage + lane * 128 + ((x ^ (lane & 7)) << 4)),
-                                         "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
-                                         : "memory");
-                        __syncwarp();
-                        uint4 w[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
-                                         : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
-                        float* part = p.partial + (2 * static_cast<int64_t>(slot) + t) * kTilePart<DP>;
-                        if (i == 0 && q == 0 && valid) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(ref, l);
-                        part += 2 * kTileRows + (32 * wq + sub) * DP + 64 * i + 32 * q + 4 * ch;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            if (valid_rows >> (4 * x) & 1) *reinterpret_cast<uint4*>(part + 4 * x * DP) = w[x];
-                        __syncwarp();
-                        continue;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = sees > 0 ? Pair16<T>::pack(__uint_as_float(o[8 * h + 2 * x]) * inv,
-                                                             __uint_as_float(o[8 * h + 2 * x + 1]) * inv)
-                                           : 0u;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         stage + lane * 128 + (((4 * q + h) ^ (lane & 7)) << 4)),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                     : "memory");
-                    }
-                }
-                if (kPaged && slot >= 0) continue;
-                __syncwarp();
-                uint4 w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
-                                 : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
-                if (64 * i + 8 * ch < p.D) {
+                    __syncwarp();
+                    float4 w[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
-                        if (valid_rows >> (4 * x) & 1) *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + to_row[x] + 64 * i) = w[x];
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(w[x].x), "=f"(w[x].y), "=f"(w[x].z), "=f"(w[x].w)
+                                     : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
+                    if (slot >= 0) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (valid_rows >> (4 * x) & 1)
+                                reinterpret_cast<float4*>(to_row[x])[8 * c + ch] = w[x];
+                    } else if (32 * c + 4 * ch < p.D) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (valid_rows >> (4 * x) & 1)
+                                reinterpret_cast<uint2*>(to_row[x])[8 * c + ch] =
+                                    make_uint2(Pair16<T>::pack(w[x].x, w[x].y), Pair16<T>::pack(w[x].z, w[x].w));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (valid && slot >= 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(ref, l);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < DP / 64; ++i) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t o[32];
+                        if (tiles > 0) {
+                            tmem_ld_32x32b_x32(to + 64 * i + 32 * q, o);
+                            tmem_wait_ld_regs32(o);
+                        }
+                        if (bad) {
+                            for (int key = edge * kKeyTile; key < lim; ++key) {
+                                const T* src = static_cast<const T*>(p.v) + static_cast<int64_t>(k0 + key) * p.v_token +
+                                               static_cast<int64_t>(hk) * p.v_head + 64 * i + 32 * q;
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) {
+                                    if (64 * i + 32 * q + x >= p.D) continue;
+                                    const float val = static_cast<float>(src[x]);
+                                    if (!isfinite(val)) o[x] = __float_as_uint(__uint_as_float(o[x]) + val);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                w[x] = lim > 0 ? Pair16<T>::pack(__uint_as_float(o[8 * h + 2 * x]) * inv,
+                                                                 __uint_as_float(o[8 * h + 2 * x + 1]) * inv)
+                                               : 0u;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             stage + lane * 128 + (((4 * q + h) ^ (lane & 7)) << 4)),
+                                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                         : "memory");
+                        }
+                    }
+                    __syncwarp();
+                    uint4 w[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
+                                     : "r"(stage + (4 * x + sub) * 128 + ((ch ^ ((4 * x + sub) & 7)) << 4)));
+                    if (64 * i + 8 * ch < p.D) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (valid_rows >> (4 * x) & 1)
+                                *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + to_row[x] + 64 * i) = w[x];
+                    }
+                    __syncwarp();
+                }
             }
             if (p.lse && valid && slot < 0)
                 p.lse[static_cast<int64_t>(q0 + token) * p.Hq + head] =
