@@ -9,8 +9,8 @@ namespace {
 
 constexpr int kMaxPairs = 128;  // heads of at most 256 elements
 
-// The angle p f in half turns, in [-1, 1).
-__device__ __forceinline__ float half_turns(int64_t p, double f) {
+// The turn per position of a frequency f (radians), as a multiple of 2^-64 turns.
+__device__ __forceinline__ uint64_t turn_step(double f) {
     // f / (2 pi) as a sum of two doubles (1 / (2 pi) = kHi + kLo), whole turns off
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
     constexpr double k64 = 18446744073709551616.0;
@@ -21,9 +21,15 @@ __device__ __forceinline__ float half_turns(int64_t p, double f) {
     t -= floor(t);
     const uint64_t step = static_cast<uint64_t>(t * k64) + static_cast<uint64_t>(static_cast<int64_t>(e * k64));
     const uint64_t back = __double_as_longlong(f) >> 63;  // all ones for a negative f
-    const uint64_t turn = ((static_cast<uint64_t>(p) ^ back) - back) * step;
+    return (step ^ back) - back;
+}
+
+// The angle at position p in half turns, in [-1, 1).
+__device__ __forceinline__ float half_turns_of(int64_t p, uint64_t step) {
+    const uint64_t turn = static_cast<uint64_t>(p) * step;
     return static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
 }
+__device__ __forceinline__ float half_turns(int64_t p, double f) { return half_turns_of(p, turn_step(f)); }
 
 }  // namespace
 }  // namespace w8a8
