@@ -29,7 +29,7 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kResident = 1024;  // threads of an SM
 constexpr int kAtOnce = 3;  // heads of a thread in flight
 constexpr int kUnits = 16;  // threads of the largest heads
 constexpr int kUnit = 20;   // floats from a thread's 16 factors to the next one's: other banks
@@ -76,8 +76,8 @@ struct Factors {
 };
 
 // lanes: threads of a head, a power of two.
-template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 8)
+template <typename T, bool kHalf, int kThreads>
+__global__ void __launch_bounds__(kThreads, kResident / kThreads)
     norm_rotary_kernel(const __grid_constant__ NormRotaryArgs a, const int lanes) {
     __shared__ uint64_t steps[kMaxPairs];
     __shared__ __align__(16) Factors factors[2];  // of this token and the one before
@@ -121,11 +121,15 @@ __global__ void __launch_bounds__(kThreads, 8)
             k_at = page * a.k_page + row * p.k_out.token;
             v_at = page * a.v_page + row * p.v_out.token;
         }
-        const int q_heads = p.q.heads, heads = q_heads + (store_k ? p.k.heads : 0);
+        // heads of Q, then of K, then of V
+        const int q_heads = p.q.heads, qk_heads = q_heads + p.k.heads;
+        const int heads = store_k ? qk_heads + p.v.heads : q_heads;
         const T* q_src = static_cast<const T*>(p.q.ptr) + t * p.q.token;
         const T* k_src = static_cast<const T*>(p.k.ptr) + t * p.k.token;
+        const T* v_src = static_cast<const T*>(p.v.ptr) + t * p.v.token;
         T* q_dst = static_cast<T*>(const_cast<void*>(p.q_out.ptr)) + t * p.q_out.token;
         T* k_dst = static_cast<T*>(const_cast<void*>(p.k_out.ptr)) + k_at;
+        T* v_dst = static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + v_at;
 
         bool ready = false;
         // (all threads of a warp take every pass: the shuffles are theirs together)
@@ -137,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, 8)
                 const int h = h0 + i * per_pass + of_pass;
                 w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
                 if (h >= heads) continue;
-                const T* src = h < q_heads ? q_src + h * p.q.head : k_src + (h - q_heads) * p.k.head;
+                const T* src = h < q_heads    ? q_src + h * p.q.head
+                               : h < qk_heads ? k_src + (h - q_heads) * p.k.head
+                                              : v_src + (h - qk_heads) * p.v.head;
                 if (has0) w0[i] = *reinterpret_cast<const uint4*>(src + c0);
                 if (has1) w1[i] = *reinterpret_cast<const uint4*>(src + c1);
             }
@@ -185,6 +191,12 @@ __global__ void __launch_bounds__(kThreads, 8)
                 for (int e = 1; e < 8; ++e) s = f2_fma(z[e], z[e], s);
                 const float r = rsqrtf(sum_of(f2_sum(s), lanes) * inv_dim + a.eps);
                 if (h >= heads || !has0) continue;
+                if (h >= qk_heads) {  // V as it is
+                    T* to = v_dst + (h - qk_heads) * p.v_out.head;
+                    *reinterpret_cast<uint4*>(to + c0) = w0[i];
+                    if (has1) *reinterpret_cast<uint4*>(to + c1) = w1[i];
+                    continue;
+                }
                 const int side = h >= q_heads, kh = side ? h - q_heads : h;
                 const HeadNorm& norm = side ? a.k_norm : a.q_norm;
                 if (norm.stride && norm.gamma) {  // a row of gamma for each head
@@ -212,16 +224,6 @@ __global__ void __launch_bounds__(kThreads, 8)
                 if (has1) *reinterpret_cast<uint4*>(to + c1) = pack8<T>(y + 4);
             }
         }
-
-        if (!p.v.ptr || !store_k) continue;
-        const T* v_src = static_cast<const T*>(p.v.ptr) + t * p.v.token;
-        T* v_dst = static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + v_at;
-        const int chunks = p.dim >> 3, all = p.v.heads * chunks;
-        for (int u = threadIdx.x; u < all; u += kThreads) {
-            const int h = u / chunks, c = 8 * (u - h * chunks);
-            *reinterpret_cast<uint4*>(v_dst + h * p.v_out.head + c) =
-                *reinterpret_cast<const uint4*>(v_src + h * p.v.head + c);
-        }
     }
 }
 
@@ -229,8 +231,11 @@ template <typename T, bool kHalf>
 cudaError_t launch(const NormRotaryArgs& a, int num_sms, cudaStream_t st) {
     int lanes = 1;
     while (16 * lanes < a.r.dim) lanes *= 2;
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(a.r.tokens, num_sms * 8));
-    norm_rotary_kernel<T, kHalf><<<ctas, kThreads, 0, st>>>(a, lanes);
+    // 64 threads where a token has no more than they keep in flight
+    const int threads = (a.r.q.heads + a.r.k.heads + a.r.v.heads) * lanes <= 64 * kAtOnce ? 64 : 128;
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(a.r.tokens, num_sms * (kResident / threads)));
+    if (threads == 64) norm_rotary_kernel<T, kHalf, 64><<<ctas, 64, 0, st>>>(a, lanes);
+    else norm_rotary_kernel<T, kHalf, 128><<<ctas, 128, 0, st>>>(a, lanes);
     return cudaGetLastError();
 }
 
