@@ -76,6 +76,8 @@ CASES = [
     ([100, 2], [1000, 77], 80, 130, 1, 8, BF16, "token"),                # a group of more heads than a tile's rows
     ([9, 17, 128], [400, 2000, 150], 16, 34, 2, 120, BF16, "token"),     # groups that do not divide the tile's rows
     ([1537], [1537], 64, 2, 1, 128, BF16, "token"),
+    ([4, 2, 6], [300, 64, 120], 16, 40, 8, 128, BF16, "head"),           # two MMA tiles of rows, few keys
+    ([31, 0, 7], [200, 5, 3], 8, 4, 4, 72, FP16, "pair"),
 ]
 
 

@@ -1,7 +1,8 @@
 // Attention of new tokens over a cache in pages.
 //
-// Where no sequence has more than 16 packed rows (queries x heads of a group), the
-// kernel of few queries (attention.cu) serves the call: the keys' bytes bound it.
+// Where no sequence has more than 16 packed rows (queries x heads of a group; 32, where
+// the table has room for few keys), the kernel of few queries (attention.cu) serves the
+// call: the keys' bytes bound it.
 // Otherwise the tensor cores do (attention_prompt.cuh), with the keys of an item cut
 // into pieces so that all SMs have the same share whatever the lengths, and sequences
 // of few and of many queries run beside each other; a second kernel joins the
@@ -128,8 +129,15 @@ cudaError_t launch_paged_attention(const AttentionArgs& args, int max_queries, i
                                    void* encode_fn, cudaStream_t st, char* detail, size_t n) {
     AttentionArgs a = args;
     a.expected_rows = max_queries * a.group;
-    // groups of more heads than a tile has rows, and caches without keys, have only the first kernel
-    if (a.expected_rows <= kFewRows || a.group > kTileRows || a.max_pages == 0)
+    // Up to 16 rows the kernel of few queries reads each key once for one MMA tile.  With
+    // two such tiles it is the better one while the table has room for few keys, as it
+    // starts and ends faster (us, 40 heads on 8 x 128, 4 queries each: 4 sequences of 500
+    // keys 13.5 against 17.5, 16 of 500 15.6 against 22; 16 of 2000 46 against 38, 4 of
+    // 8000 46 against 36).  Groups of more heads than a tile has rows, and caches without
+    // keys, have only that kernel.
+    const double keys = static_cast<double>(a.batch) * a.Hk * a.max_pages * a.page_size;
+    const bool few = a.expected_rows <= kFewRows || (a.expected_rows <= 2 * kFewRows && keys <= 98304);
+    if (few || a.group > kTileRows || a.max_pages == 0)
         return launch_attention_split(a, dtype, num_sms, workspace, encode_fn, st, detail, n);
     uint8_t* at = static_cast<uint8_t*>(workspace) + attention_workspace_bytes(num_sms);
     a.joins = at;

@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= kSoftmaxWarps) {
-        regs_dec<kPaged ? 80 : 72>();  // (of 168 a thread at launch: 8 warps of 208 and 4 of 80)
+        regs_dec<kPaged ? 88 : 72>();  // (168 a thread at launch: 8 warps of 208 and 4 of 88)
         if (warp == kSoftmaxWarps + 1) {
             // ---- items and TMA loads: K_0 Q_0 Q_1 K_1 V_0 ...
             if (!kPaged && elect_one_sync()) {
