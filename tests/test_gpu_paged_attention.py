@@ -99,6 +99,31 @@ def test_paged_attention(w8a8, n, m, page, hq, hk, d, dtype, layout, causal):
     assert w8a8.get_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("n,m,page,hq,hk,d,dtype", [
+    ([300], [9000], 48, 8, 8, 128, BF16), ([260, 150], [8700, 9999], 64, 32, 8, 128, FP16), ([513], [17000], 16, 16, 8, 64, BF16),
+    ([70], [16500], 256, 24, 4, 128, BF16), ([1300], [8500], 40, 8, 8, 128, BF16)])
+def test_many_keys_and_rows(w8a8, n, m, page, hq, hk, d, dtype):
+    """Caches that fill a good part of L2 (where pieces do not begin with their first key
+    tile), with values that are not finite among keys that only the last rows see."""
+    c = Paged(m, page, hk, d, dtype, 81)
+    q = queries(sum(n), hq, d, dtype, 82)
+    call = lambda: w8a8.paged_attention(q, c.k_pages, c.v_pages, c.table, c.k_lens, cu_q=starts(n), lse=True)
+    o, lse = call()
+    check(o, lse, q, *c.flat(), n, m, True, d ** -0.5)
+    for _ in range(5):
+        again = call()
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    at = m[0] - n[0] // 2
+    c.v_pages[int(c.table[0, at // page]), at % page] = math.inf
+    o, lse = call()
+    first = n[0] - n[0] // 2
+    check(o[:first], lse[:first], q[:first], c.k[0][:at], c.v[0][:at], [first], [at], True, d ** -0.5)
+    assert not torch.isfinite(o[first:n[0]]).any()
+    for b in range(1, len(n)):
+        check(o[n[0]:], lse[n[0]:], q[n[0]:], c.k[b], c.v[b], n[1:], m[1:], True, d ** -0.5)
+    assert w8a8.get_device_error() == (0, 0)
+
+
 def test_the_most_queries_need_not_be_true(w8a8):
     n, m = [1, 90, 5], [500, 600, 700]
     c = Paged(m, 32, 2, 64, BF16, 3)

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
             const int t_end = piece_end(), hg = c.item / c.blocks, rb = c.item - hg * c.blocks;
             const int end = seen_end(rb, t_end), hk = hg * p.side_heads + side;
             Boxes<kTile> boxes;
-            if (kPaged && c.tile < end) boxes.start(p, c.b, c.s.m, c.tile);
+            if (kPaged && c.tile < end) boxes.start(p, c.b, c.s.m, c.tile, end - c.tile, 0);
             for (int t = c.tile; t < end; ++t) {
                 if (kPaged) boxes.step(p);
                 ok = mbar_wait(&empty[st], ph ^ 1, 50);

@@ -101,6 +101,7 @@ struct Boxes {
     int key, index, row;  // of this lane's box of the next tile
     int pages, rest;      // a tile's keys by the page, and what is left of them
     int m, b;
+    int left, first_key, first_index, first_row;  // tiles up to the last; the box of the first
     unsigned entry;       // of the next tile's box
     int page, at_row;     // of the present one's
 
@@ -108,14 +109,25 @@ struct Boxes {
         entry = ~0u;  // past the keys: no page
         if (threadIdx.x % 32 < boxes && key < m) entry = entry_of(p, b, index);
     }
-    // before key tile `tile` of sequence `seq` with `keys` keys
-    __device__ __forceinline__ void start(const AttentionArgs& p, int seq, int keys, int tile) {
+    __device__ __forceinline__ void place(const AttentionArgs& p) {
+        index = static_cast<unsigned>(key) / static_cast<unsigned>(p.page_size);
+        row = key - index * p.page_size;
+    }
+    // for `count` tiles of sequence `seq` with `keys` keys: tiles first + turn, ... to the
+    // last, then from `first` on
+    __device__ __forceinline__ void start(const AttentionArgs& p, int seq, int keys, int first, int count, int turn) {
         boxes = kTile / p.box;
         b = seq;
         m = keys;
-        key = tile * kTile + static_cast<int>(threadIdx.x % 32) * p.box;
-        index = static_cast<unsigned>(key) / static_cast<unsigned>(p.page_size);
-        row = key - index * p.page_size;
+        first_key = key = first * kTile + static_cast<int>(threadIdx.x % 32) * p.box;
+        place(p);
+        first_index = index;
+        first_row = row;
+        if (turn > 0) {
+            key += turn * kTile;
+            place(p);
+        }
+        left = count - turn;
         pages = kTile / p.page_size;
         rest = kTile - pages * p.page_size;
         look_up(p);
@@ -130,6 +142,11 @@ struct Boxes {
         if (row >= p.page_size) {
             row -= p.page_size;
             ++index;
+        }
+        if (--left == 0) {
+            key = first_key;
+            index = first_index;
+            row = first_row;
         }
         look_up(p);
     }

@@ -102,6 +102,11 @@ struct Item {
     int slot;           // where its partial result goes; -1: the piece is all there is
     int last_tile;      // of the whole item
     int seen;           // keys of the sequence that every row sees
+    int turn;           // the first of its key tiles to be taken, at most `edge`; they go round
+    // key tile of step j
+    __device__ __forceinline__ static int tile_of(int j, int turn, int keys) {
+        return j + turn < keys ? j + turn : j + turn - keys;
+    }
 };
 
 // What the join of an item's pieces needs of it: a seat for each piece, two a CTA
@@ -304,11 +309,12 @@ struct Items {
 // each tile of rows, and an item's end kEnds.
 struct Pieces {
     static constexpr int kEnds = 6;
-    int64_t w, w_end, per, item_start;
-    int b, blocks, groups, hg, block, at;  // at: in the item's part of the line
+    int64_t w, w_end, per, item_start;     // what is left of the range: [w, w_end)
+    int b, blocks, groups, hg, block, at;  // at: where w_end is in the item's part of the line
     int tiles, each, line;                 // the item's key tiles, units of one, its part of the line
     Sequence s;
     int pair_tokens, side, range;
+    int passed;                            // key tiles of this CTA so far
 
     __device__ __forceinline__ int limit(const AttentionArgs& p, const Sequence& q, int token) const {
         return p.causal ? clampi(token + q.m - q.n + 1, 0, q.m) : q.m;
@@ -373,8 +379,9 @@ struct Pieces {
         per = max(static_cast<int64_t>(2 + kEnds), quotient(total + ranges - 1, ranges));
         w = per * range;
         w_end = min(total, w + per);
+        passed = 0;
         if (w >= w_end) return false;
-        int64_t left = w;
+        int64_t left = w_end - 1;
         for (int b0 = 0;; b0 += 32) {
             if (b0 > 0) lines(p, b0, mine, incl);
             const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
@@ -407,7 +414,7 @@ struct Pieces {
             if (hit) {
                 const int l = __ffs(hit) - 1;
                 block = i0 + l;
-                at = static_cast<int>(left) - __shfl_sync(0xffffffffu, sum - one, l);
+                at = static_cast<int>(left) - __shfl_sync(0xffffffffu, sum - one, l) + 1;
                 break;
             }
             left -= __shfl_sync(0xffffffffu, sum, 31);
@@ -416,30 +423,28 @@ struct Pieces {
         return true;
     }
 
-    __device__ __forceinline__ bool next_item(const AttentionArgs& p) {
-        at = 0;
-        if (++block == blocks) {
-            block = 0;
-            if (++hg == groups) {
-                hg = 0;
+    __device__ __forceinline__ void previous_item(const AttentionArgs& p) {
+        if (--block < 0) {
+            if (--hg < 0) {
                 do {
-                    if (++b >= p.batch) return false;
-                    s = sequence<true>(p, b);
+                    s = sequence<true>(p, --b);
                     blocks = blocks_of(s);
                 } while (blocks == 0);
+                hg = groups - 1;
             }
+            block = blocks - 1;
         }
         item(p);
-        return true;
+        at = line;
     }
 
-    // The next piece; any = 0 at the end.
+    // The next piece, from the range's end to its beginning; any = 0 when there is none.
     __device__ __forceinline__ Item next(const AttentionArgs& p) {
         Item it{};
         while (w < w_end) {
-            const int end = static_cast<int>(min(static_cast<int64_t>(line), at + (w_end - w)));
+            const int begin = static_cast<int>(max(static_cast<int64_t>(0), at - (w_end - w)));
             // a key tile belongs to the range that its first unit lies in
-            const int most = max(tiles, 1), from = (at + each - 1) / each, to = min((end + each - 1) / each, most);
+            const int most = max(tiles, 1), from = (begin + each - 1) / each, to = min((at + each - 1) / each, most);
             const bool some = from < to;
             if (some) {
                 it.any = 1;
@@ -455,15 +460,37 @@ struct Pieces {
                 it.seen = limit(p, s, it.token0);
                 it.edge = clampi(it.seen / kKeyTile - from, 0, it.keys);
                 it.slot = from == 0 && to == most ? -1 : 2 * blockIdx.x + (from == 0);
-                item_start = w - at;
+                item_start = w_end - at;
                 it.last_tile = most - 1;
+                if (turns(p)) it.turn = min(turn(from, it.keys), it.edge);
+                passed += it.keys + kEnds / 2;
             }
-            w += end - at;
-            at = end;
-            if (at == line && w < w_end && !next_item(p)) w = w_end;
+            w_end -= at - begin;
+            at = begin;
+            if (at == 0 && w < w_end) previous_item(p);
             if (some) break;
         }
         return it;
+    }
+
+    // Where a piece begins with its key tiles, so that the CTAs that take the items of one
+    // KV head (whose pieces lie in different places) pass the same keys at about the same
+    // time and find them in L2: fronts as far apart as a CTA gets, that all started with
+    // the call.  (A range that begins in one item and ends in the next takes the end first:
+    // those are the next item's first keys.)  Where the items of a sequence are about as
+    // long as each other and its keys fill a good part of L2: 512 tokens, 40 heads on 8 x
+    // 128, over 33280 keys 275 -> 256 us, over 131072 1010 -> 890, over 8192 99 -> 93; the
+    // items of a whole prompt, which differ, lose 2%.
+    __device__ __forceinline__ bool turns(const AttentionArgs& p) const {
+        return blocks > 1 && 4 * tiles >= 3 * tiles_of(p, s, blocks - 1) &&
+               static_cast<int64_t>(s.m) * p.Hk * p.D * 4 >= (int64_t{32} << 20);
+    }
+    __device__ __forceinline__ int turn(int from, int keys) const {
+        const int range_tiles = max(1, static_cast<int>(per >> (each - 1)));
+        const int fronts = max(1, (tiles + range_tiles / 2) / range_tiles), apart = max(1, tiles / fronts);
+        int ahead = (passed - from) % apart;
+        if (ahead < 0) ahead += apart;
+        return ahead < keys ? ahead : 0;
     }
 
     // The seat of a piece at its item's join: the ranges in which its first and its
@@ -582,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!kPaged && lane == 0) index = atomicAdd(p.counters, 1);
                 const int jmax = it.keys;
                 Boxes<kKeyTile> boxes;
-                if (kPaged && jmax > 0) boxes.start(p, it.b, it.m, it.j0);
+                if (kPaged && jmax > 0) boxes.start(p, it.b, it.m, it.j0, jmax, it.turn);
                 for (int i = 0; i < 2 * jmax; ++i) {
                     const int j = load_tile(i, jmax);
                     const bool is_v = load_is_v(i, jmax);
@@ -657,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Ring<S> r;  // the item's first load
                 bool ok = true;
                 // all steps of an item with kT tiles
-                auto run = [&](auto tc, int J, int edge) {
+                auto run = [&](auto tc, int J, int edge, int past) {
                     constexpr int kT = decltype(tc)::value;
                     Ring<S> rk = r, rv = r;  // the next K and V to use
                     rv.next(load_of_v(0, J));
@@ -689,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_ph ^= (1 << kT) - 1;
                     for (int j = 0; j < J; ++j) {
                         if (!(ok = mbar_wait(&bars->kv_full[rv.st], rv.ph, 66))) return;
-                        if (j >= edge) {
+                        if (j >= edge && (!kPaged || j < past)) {
                             if (!(ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67))) return;
                             ++edges;
                         }
@@ -719,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 // a tile alone: its key tiles go to O of tile 0 and of tile 1 in turn
-                auto run_alone = [&](int J, int edge) {
+                auto run_alone = [&](int J, int edge, int past) {
                     Ring<S> rk = r, rv = r;
                     rv.next(load_of_v(0, J));
                     auto scores = [&](int j, int to) {
@@ -745,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_ph ^= 1;
                     for (int j = 0; j < J; ++j) {
                         if (!(ok = mbar_wait(&bars->kv_full[rv.st], rv.ph, 66))) return;
-                        if (j >= edge) {
+                        if (j >= edge && j < past) {
                             if (!(ok = mbar_wait(&bars->v_clean[edges & 3], (edges >> 2) & 1, 67))) return;
                             ++edges;
                         }
@@ -776,13 +803,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int at = 0; ok; ++at) {
                     if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 63)) break;
                     const volatile Item& it = bars->items[at & 1];
-                    const int any = it.any, two = it.tiles > 1, J = it.keys, edge = it.edge;
+                    const int any = it.any, two = it.tiles > 1, J = it.keys, turn = kPaged ? it.turn : 0;
+                    const int edge = it.edge - turn, past = J - turn;  // steps of the tiles from edge on
                     if (!any) break;
                     mbar_arrive(&bars->item_empty[at & 1]);
                     if (J == 0) continue;
-                    if (two) run(std::integral_constant<int, 2>{}, J, edge);
-                    else if (kPaged) run_alone(J, edge);
-                    else run(std::integral_constant<int, 1>{}, J, edge);
+                    if (two) run(std::integral_constant<int, 2>{}, J, edge, past);
+                    else if (kPaged) run_alone(J, edge, past);
+                    else run(std::integral_constant<int, 1>{}, J, edge, past);
                     r.skip(2 * J);
                 }
             // every commit has arrived before the CTA ends
@@ -800,14 +828,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(&bars->item_full[at & 1], (at >> 1) & 1, 81)) break;
                 const volatile Item& it = bars->items[at & 1];
                 if (!it.any) break;
-                const int jmax = it.keys, hk = it.hk, edge = it.edge;
+                const int jmax = it.keys, hk = it.hk, edge = it.edge, turn = it.turn;
                 Boxes<kKeyTile> boxes;
-                if (jmax > 0) boxes.start(p, it.b, it.m, it.j0);
+                if (jmax > 0) boxes.start(p, it.b, it.m, it.j0, jmax, turn);
                 leave_item(at);
                 for (int i = 0; i < 2 * jmax; ++i, r.next()) {
                     if (!load_is_v(i, jmax)) continue;
                     ok = mbar_wait(&bars->kv_empty[r.st], r.ph, 82);
                     if (!ok) break;
+                    const int j = load_tile(i, jmax), tile = Item::tile_of(j, turn, jmax);
                     boxes.step(p);
                     if (elect_one_sync()) mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTileBytes);
                     boxes.each([&](int x, int row, int page) {
@@ -816,10 +845,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < L::kChunks; ++c)
                             tma_load_page(dst + c * kChunkBytes, &tmV, &bars->kv_full[r.st], 64 * c, hk, row, page);
                     });
-                    const int j = load_tile(i, jmax);
-                    if (j >= edge && elect_one_sync()) mbar_arrive(&bars->v_issued[(edges + j - edge) & 3]);
+                    if (tile < edge) continue;
+                    if (elect_one_sync()) mbar_arrive(&bars->v_issued[edges & 3]);
+                    ++edges;
                 }
-                edges += max(0, jmax - edge);
             }
             for (int i = 0; i < S; ++i) {  // nothing is in flight when the CTA ends
                 mbar_wait(&bars->kv_full[r.st], r.ph, 82);
@@ -836,7 +865,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 volatile Item& it = bars->items[at & 1];
                 if (!it.any) break;
                 const int jmax = it.keys;
-                for (int j = it.edge; j < jmax && ok; ++j, ++edges) {
+                for (int j = kPaged ? 0 : it.edge; j < jmax && ok; ++j) {
+                    const int tile = kPaged ? Item::tile_of(j, it.turn, jmax) : j;
+                    if (tile < it.edge) continue;
                     const int lv = ld + load_of_v(j, jmax);
                     ok = mbar_wait(&bars->v_issued[edges & 3], (edges >> 2) & 1, 72) &&
                          mbar_wait(&bars->kv_full[lv % S], (lv / S) & 1, 73);
@@ -847,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c0 = me; c0 < L::kTileBytes / 16; c0 += kCleaners * kAtOnce) {
                         // 32 keys at a time, from those on that some row does not see
                         static_assert(!kPaged || kCleaners * kAtOnce == 32 * 8, "32 keys");
-                        if (kPaged && (it.j0 + j) * kKeyTile + ((c0 - me) / 8 & 127) + 32 <= it.seen) continue;
+                        if (kPaged && (it.j0 + tile) * kKeyTile + ((c0 - me) / 8 & 127) + 32 <= it.seen) continue;
                         uint4 w[kAtOnce];
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i)
@@ -872,13 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v + 16 * c), "r"(u[0]),
                                          "r"(u[1]), "r"(u[2]), "r"(u[3])
                                          : "memory");
-                            const int key = (kPaged ? it.j0 + j : j) * kKeyTile + ((c >> 3) & 127);
+                            const int key = (kPaged ? it.j0 + tile : j) * kKeyTile + ((c >> 3) & 127);
                             if (key < it.m) it.bad = 1;
                         }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->v_clean[edges & 3]);
+                    ++edges;
                 }
                 ld += 2 * jmax;
                 leave_item(at);
@@ -920,6 +952,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const int tiles = alone || t < both ? it.keys : 0;
+            // first key of the step's tile, from the item's first one
+            int key0 = kPaged ? Item::tile_of(j_first, it.turn, it.keys) * kKeyTile : 0;
             float ref = -INFINITY;
             auto base_of = [](float r) { return r == -INFINITY ? 0.0f : kShift<T> - r; };
             uint64_t sum2 = f2_pack(0.0f, 0.0f);
@@ -934,10 +968,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_wait_ld_regs32(v[i]);
-                if (warp_lim < (j + 1) * kKeyTile) {
+                if (!kPaged) key0 = j * kKeyTile;
+                if (warp_lim < key0 + kKeyTile) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int left = lim - j * kKeyTile - 32 * i;  // columns this row sees
+                        const int left = lim - key0 - 32 * i;  // columns this row sees
                         if (!__any_sync(0xffffffffu, left < 32)) continue;
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -999,6 +1034,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 sum2 = f2_add(part2[0], part2[1]);
+                if (kPaged) {
+                    key0 += j_step * kKeyTile;
+                    if (key0 >= tiles * kKeyTile) key0 -= tiles * kKeyTile;
+                }
             }
 
             steps = (steps + both * it.keys) % L::kBuffers;
