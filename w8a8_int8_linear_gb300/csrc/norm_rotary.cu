@@ -12,7 +12,10 @@
 //
 // Bytes bound it.  A CTA takes a token at a time, so that few tokens go to as many
 // SMs; the turn per position of each frequency, which takes 64-bit floating point,
-// is computed once per CTA.
+// is computed once per CTA (gamma, cos and sin from their own places for every head,
+// and the 64-bit steps for every token: 67.5 us against 57).  16384 tokens x 40 heads of
+// 128 take 57 us (0.87 of the copy bandwidth; x 48 heads 65, 0.93), 8000 tokens of 32
+// heads on 8 into pages 35, 48 single tokens 4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
