@@ -453,7 +453,7 @@ W8A8_API w8a8_status w8a8_qk_norm_rotary_append(
  * j / page_size].
  *   K_pages, V_pages [pages,page_size,Hk,D]: page, token and head strides in
  *   elements (positive multiples of 8 below 2^39); page_size % 8 == 0, at most
- *   2^20.
+ *   2^20, and max_pages * page_size < 2^31 - 1024.
  *   page_table [batch,max_pages] int32 (device), rows table_stride apart.  An
  *   entry outside [0, pages) reads as a page of zeros; entries past the last
  *   page of a sequence are not read.

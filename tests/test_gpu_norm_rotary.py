@@ -162,3 +162,34 @@ def test_rows_past_32_bits(w8a8):
     w8a8.qk_norm_rotary_append(q, k, v, pos, freqs, kc, vc, slots)
     _, k1 = w8a8.qk_norm_rotary(q, k, pos, freqs)
     assert torch.equal(kc.flatten(0, 1)[slots], k1) and torch.equal(vc.flatten(0, 1)[slots], v)
+
+
+def test_nothing_to_do(w8a8):
+    freqs = w8a8.rotary_frequencies(64)
+    z = torch.empty(0, dtype=torch.int64, device=DEV)
+    x = torch.empty(0, 4, 64, dtype=BF16, device=DEV)
+    q, k = w8a8.qk_norm_rotary(x, x, z, freqs)
+    assert q.shape == k.shape == (0, 4, 64)
+    cache = torch.zeros(2, 8, 4, 64, dtype=BF16, device=DEV)
+    assert w8a8.qk_norm_rotary_append(x, x, x, z, freqs, cache, cache.clone(), z).shape == (0, 4, 64)
+    # no query heads: only K and V
+    one = torch.zeros(1, dtype=torch.int64, device=DEV)
+    none, kv = torch.empty(1, 0, 64, dtype=BF16, device=DEV), torch.randn(1, 4, 64, device=DEV).to(BF16)
+    kc, vc = cache.clone(), cache.clone()
+    assert w8a8.qk_norm_rotary_append(none, kv, kv, one + 1, freqs, kc, vc, one + 9).shape == (1, 0, 64)
+    assert torch.equal(vc[1, 1], kv[0]) and torch.equal(kc[1, 1], w8a8.qk_norm_rotary(kv, None, one + 1, freqs)[0][0])
+    # a cache of no rows is refused, as by rotary_append
+    empty = cache[:0]
+    with pytest.raises(w8a8.W8A8Error):
+        w8a8.qk_norm_rotary_append(kv, kv, kv, one, freqs, empty, empty.clone(), one)
+
+
+def test_values_of_v_are_copied_bit_for_bit(w8a8):
+    freqs = w8a8.rotary_frequencies(64)
+    bits = torch.randint(-32768, 32768, (40, 2, 64), dtype=torch.int16, device=DEV)
+    v = bits.view(BF16)
+    kc, vc = (torch.zeros(3, 16, 2, 64, dtype=BF16, device=DEV) for _ in range(2))
+    k = torch.randn(40, 2, 64, device=DEV).to(BF16)
+    slots = torch.randperm(48, device=DEV)[:40]
+    w8a8.qk_norm_rotary_append(k, k, v, slots, freqs, kc, vc, slots)
+    assert torch.equal(vc.flatten(0, 1)[slots].view(torch.int16), bits)

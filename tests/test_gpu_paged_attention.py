@@ -78,6 +78,10 @@ CASES = [
     ([1537], [1537], 64, 2, 1, 128, BF16, "token"),
     ([4, 2, 6], [300, 64, 120], 16, 40, 8, 128, BF16, "head"),           # two MMA tiles of rows, few keys
     ([31, 0, 7], [200, 5, 3], 8, 4, 4, 72, FP16, "pair"),
+    ([3, 9, 1], [700, 40, 1], 32, 100, 1, 64, BF16, "token"),            # one query a tile, rows to spare
+    ([3, 1, 2], [700, 40, 129], 32, 256, 2, 128, FP16, "head"),          # and none to spare
+    ([40, 1, 3], [900, 2000, 3], 24, 14, 7, 48, BF16, "token"),          # seven KV heads
+    ([40, 1, 3], [900, 2000, 3], 24, 11, 11, 128, BF16, "pair"),         # a prime number of them
 ]
 
 
@@ -305,6 +309,70 @@ def test_a_table_shared_by_all(w8a8):
                                   torch.tensor(lens, dtype=torch.int32, device=DEV), lse=True)
     k, v = (torch.cat([x[0][:m] for m in lens]) for x in (c.k, c.v))
     check(o, lse, q, k, v, [1] * 4, lens, True, 0.125)
+
+
+def test_thousands_of_sequences(w8a8):
+    """More sequences than a warp counts at once, two of them with many queries, without a word about it."""
+    n = [1] * 3000
+    n[0], n[1700], n[2999] = 37, 150, 2
+    m = [q + (i * 37) % 150 for i, q in enumerate(n)]
+    c = Paged(m, 16, 1, 64, BF16, 91)
+    q = queries(sum(n), 4, 64, BF16, 92)
+    o, lse = w8a8.paged_attention(q, c.k_pages, c.v_pages, c.table, c.k_lens, cu_q=starts(n), lse=True)
+    k, v = c.flat()
+    cq, ck = starts(n).tolist(), starts(m).tolist()
+    for b in [0, 1, 31, 32, 33, 1699, 1700, 1701, 2047, 2998, 2999] + list(range(100, 3000, 97)):
+        rows, keys = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+        check(o[rows], lse[rows], q[rows], k[keys], v[keys], [n[b]], [m[b]], True, 0.125)
+    assert torch.isfinite(o).all()
+    alone = [i for i, x in enumerate(n) if x == 1]
+    rows = starts(n).long()[:-1][torch.tensor(alone, device=DEV)]
+    o1 = w8a8.paged_attention(q[rows], c.k_pages, c.v_pages, c.table[alone], c.k_lens[alone], max_queries=1)
+    assert (o1.double() - o[rows].double()).abs().max() <= 4 * 2.0 ** -8 * 4
+
+
+@pytest.mark.parametrize("n", [1, 45])
+def test_a_million_keys(w8a8, n):
+    """Pages that come again and again: what the same keys give once."""
+    c = Paged([256], 64, 2, 64, BF16, 95)
+    times = 4096
+    q = queries(n, 16, 64, BF16, 96)
+    table = c.table[:, :4].repeat(1, times)
+    lens = torch.tensor([256 * times], dtype=torch.int32, device=DEV)
+    o, lse = w8a8.paged_attention(q, c.k_pages, c.v_pages, table, lens, causal=False, lse=True)
+    want, lse1 = w8a8.paged_attention(q, c.k_pages, c.v_pages, c.table, c.k_lens, causal=False, lse=True)
+    # sums of 2^20 terms in binary32, in parts: at most 2^-24 of the total for each of the 2^20 / 16 additions of one lane
+    tol = 2.0 ** -8 * (want.double().abs() + 2.0 ** -4) + 2.0 ** -8 * c.v[0].double().abs().mean()
+    assert ((o.double() - want.double()).abs() <= tol).all()
+    assert (lse - lse1 - math.log(times)).abs().max() <= 2.0 ** -8
+
+
+def test_two_streams_at_once(w8a8):
+    n, m = [120, 1, 1, 30], [3000, 2500, 40, 900]
+    sides, want, cases = [torch.cuda.Stream() for _ in range(2)], [], []
+    for i in range(2):
+        c = Paged(m, 16, 4, 128, BF16, 101 + i)
+        cases.append((queries(sum(n), 16, 128, BF16, 103 + i), c.k_pages, c.v_pages, c.table, c.k_lens, starts(n)))
+        want.append(w8a8.paged_attention(*cases[i]))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i in range(2):
+            with torch.cuda.stream(sides[i]):
+                got[i].append(w8a8.paged_attention(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o, want[i])
+    assert w8a8.get_device_error() == (0, 0)
+
+
+def test_one_query_for_all_sequences(w8a8):
+    """A broadcast Q: the same query row for every sequence."""
+    c = Paged([100, 7, 300], 16, 2, 64, BF16, 111)
+    q = queries(1, 8, 64, BF16, 112)
+    o, lse = w8a8.paged_attention(q.expand(3, -1, -1), c.k_pages, c.v_pages, c.table, c.k_lens, lse=True)
+    check(o, lse, q.repeat(3, 1, 1), *c.flat(), [1, 1, 1], [100, 7, 300], True, 0.125)
 
 
 def test_refusals(w8a8):

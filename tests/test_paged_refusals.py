@@ -39,7 +39,7 @@ def test_paged_attention(L):
                dict(Q=None), dict(K=None), dict(V=None), dict(O=None), dict(table=None), dict(lens=None)):
         assert paged(L, **kw) == INVALID, kw
     for kw in (dict(D=12), dict(D=136), dict(Hq=5), dict(batch=3), dict(Tq=1 << 31), dict(page_size=12),
-               dict(page_size=(1 << 20) + 8), dict(page_size=1 << 16, max_pages=1 << 15), dict(pages=1 << 31),
+               dict(page_size=(1 << 20) + 8), dict(page_size=1 << 16, max_pages=1 << 15), dict(page_size=1024, max_pages=(1 << 21) - 1), dict(pages=1 << 31),
                dict(Hq=70000, Hk=1), dict(batch=1 << 31), dict(table_stride=1 << 31)):
         assert paged(L, **kw) == SHAPE, kw
     for i in range(10):

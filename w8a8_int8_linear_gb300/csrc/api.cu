@@ -923,7 +923,8 @@ w8a8_status w8a8_paged_attention(
     if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || batch > INT32_MAX ||
         Tq * (Hq / Hk) > INT32_MAX)
         return W8A8_ERR_SHAPE;
-    if (page_size % 8 != 0 || page_size > (1 << 20) || pages >= INT32_MAX || max_pages > INT32_MAX / page_size ||
+    if (page_size % 8 != 0 || page_size > (1 << 20) || pages >= INT32_MAX ||
+        max_pages > (INT32_MAX - 1024) / page_size ||  // (a key tile may end behind the last key)
         table_stride > INT32_MAX)
         return W8A8_ERR_SHAPE;
     if (batch == 0 || Tq == 0) return W8A8_OK;

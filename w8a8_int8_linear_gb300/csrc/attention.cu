@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     };
     auto piece_end = [&]() { return static_cast<int>(min(static_cast<int64_t>(c.tiles), c.tile + (w_end - w))); };
     // keys that packed row pr of the sequence sees: [0, limit)
-    auto limit = [&](int pr) { return p.causal ? clampi(pr / p.group + c.s.m - c.s.n + 1, 0, c.s.m) : c.s.m; };
+    auto limit = [&](int pr) { return p.causal ? clampi(pr / p.group - c.s.n + c.s.m + 1, 0, c.s.m) : c.s.m; };
     // tiles of the piece that some row sees end here
     auto seen_end = [&](int rb, int t_end) {
         const int last = min((rb + 1) * R, c.s.n * p.group) - 1;

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) join_kernel(const AttentionAr
                 o = make_float4(o.x * f + v[i].x * w, o.y * f + v[i].y * w, o.z * f + v[i].z * w, o.w * f + v[i].w * w);
             }
         }
-        const bool sees = !p.causal || token + it.m - it.n >= 0;  // (a joined item has keys)
+        const bool sees = !p.causal || token - it.n + it.m >= 0;  // (a joined item has keys)
         const float inv = sees ? __frcp_rn(l) : 0.0f;
         const int head = it.hk * p.group + r % p.group;
         const int64_t at = it.q0 + token;

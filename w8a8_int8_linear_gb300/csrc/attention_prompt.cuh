@@ -324,7 +324,7 @@ struct Pieces {
     int passed;                            // key tiles of this CTA so far
 
     __device__ __forceinline__ int limit(const AttentionArgs& p, const Sequence& q, int token) const {
-        return p.causal ? clampi(token + q.m - q.n + 1, 0, q.m) : q.m;
+        return p.causal ? clampi(token - q.n + q.m + 1, 0, q.m) : q.m;
     }
     __device__ __forceinline__ int tiles_of(const AttentionArgs& p, const Sequence& q, int i) const {
         return (limit(p, q, min((i + 1) * pair_tokens, q.n) - 1) + kKeyTile - 1) / kKeyTile;
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 const int n = it.n, m = it.m, token = it.token0 + my_token;
                 const bool valid = used && (alone || t < both) && token < n;
-                lim = valid ? (p.causal ? clampi(token + m - n + 1, 0, m) : m) : 0;
+                lim = valid ? (p.causal ? clampi(token - n + m + 1, 0, m) : m) : 0;
                 warp_lim = __reduce_min_sync(0xffffffffu, valid ? lim : m);
                 sees = lim;
                 if (kPaged) {
