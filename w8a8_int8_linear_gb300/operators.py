@@ -216,7 +216,7 @@ def paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q=None, max_quer
     it only spares the kernel that would serve more.  causal, scale, out and lse as
     in `attention`; rows of no sequence are not written.
 
-    The workspace (`paged_attention_workspace()`) is by default one per
+    The workspace (`paged_attention_workspace()`, 51 MB) is by default one per
     stream, kept until the process ends, and one of its own, in the graph's
     memory, for a captured call."""
     r = (_binding or binding()).paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q, max_queries, causal,
