@@ -186,7 +186,12 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     // join 0.08 us a piece for each of its rounds over the rows: few tiles are not cut
     // into more pieces than that is worth (12 heads on 1, one sequence of 4871 keys 14
     // us against 24).
-    const int least = max(1, static_cast<int>(sqrt_approx(0.23f * 16 / R * p.join_rounds * __reduce_max_sync(0xffffffffu, most))));
+    const int longest = __reduce_max_sync(0xffffffffu, most);
+    int least = max(1, static_cast<int>(sqrt_approx(0.23f * 16 / R * p.join_rounds * longest)));
+    // Over pages few tiles are not cut at all, as a join takes 2 us by itself (3 sequences
+    // of 1 to 130 keys 6.8 us against 8.1, 8 of 300 8.5 against 9.5; one of 500, which is
+    // cut, 9.2 against 10.2).
+    if (kPaged && longest <= 7) least = longest;
     int64_t per = max(static_cast<int64_t>(least), quotient(total + ranges - 1, ranges));
     // A CTA whose range ends one item and begins another takes 3 us longer: where
     // there are few tiles, ranges of a few more that start with the items are better
@@ -625,20 +630,22 @@ cudaError_t launch_split_rows(const CUtensorMap (&map)[2], const AttentionArgs& 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R, G, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SplitSmem<DP, R, G>::kTotal);
+        e = cudaFuncSetAttribute(attention_split_kernel<T, DP, R, G, kPaged>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SplitSmem<DP, R, G>::kTotal);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
     const int ctas = (3 - G) * num_sms / a.side_heads * a.side_heads;
-    attention_split_kernel<T, DP, R, G, kPaged><<<ctas, threads_of(G), SplitSmem<DP, R, G>::kTotal, st>>>(map[0], map[1], a);
+    attention_split_kernel<T, DP, R, G, kPaged>
+        <<<ctas, threads_of(G), SplitSmem<DP, R, G>::kTotal, st>>>(map[0], map[1], a);
     return cudaGetLastError();
 }
 
 template <typename T, int DP, bool kPaged>
 cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, int num_sms, cudaStream_t st) {
     // as many rows an item as a sequence has, so that its keys are read once
-    const int64_t rows = kPaged ? a.expected_rows * static_cast<int64_t>(a.batch) : static_cast<int64_t>(a.Tq) * a.group;
+    const int64_t rows = kPaged ? a.expected_rows * static_cast<int64_t>(a.batch)
+                                : static_cast<int64_t>(a.Tq) * a.group;
     if (rows <= 16 * static_cast<int64_t>(a.batch)) {
         // Two CTAs per SM where they get several items each: one starts and ends an
         // item while the other's keys stream (us, against one CTA, at heads of 128, 8
@@ -647,7 +654,8 @@ cudaError_t launch_split(const CUtensorMap (&map)[2], const AttentionArgs& a, in
         // into twice as many pieces (16 of 8192 86 against 84, on 1 KV head 27 against
         // 24, 4 of 500 9.8 against 9.5).
         const int64_t items = static_cast<int64_t>(a.batch) * (a.Hk / a.side_heads);
-        if (2 * items >= 3 * (num_sms / a.side_heads)) return launch_split_rows<T, DP, 16, 1, kPaged>(map, a, num_sms, st);
+        if (2 * items >= 3 * (num_sms / a.side_heads))
+            return launch_split_rows<T, DP, 16, 1, kPaged>(map, a, num_sms, st);
         return launch_split_rows<T, DP, 16, 2, kPaged>(map, a, num_sms, st);
     }
     if (rows <= 32 * static_cast<int64_t>(a.batch)) return launch_split_rows<T, DP, 32, 2, kPaged>(map, a, num_sms, st);

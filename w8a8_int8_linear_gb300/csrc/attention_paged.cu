@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kJoinThreads, 8) join_kernel(const AttentionAr
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 const float to = fmaxf(top, stats[i].x);
-                const float f = top == to ? 1.0f : exp2_approx(top - to), w = stats[i].x == to ? 1.0f : exp2_approx(stats[i].x - to);
+                const float f = top == to ? 1.0f : exp2_approx(top - to);
+                const float w = stats[i].x == to ? 1.0f : exp2_approx(stats[i].x - to);
                 top = to;
                 l = l * f + stats[i].y * w;
                 o = make_float4(o.x * f + v[i].x * w, o.y * f + v[i].y * w, o.z * f + v[i].z * w, o.w * f + v[i].w * w);
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(kJoinThreads, 8) join_kernel(const AttentionAr
                 sees ? make_uint2(Pair16<T>::pack(o.x * inv, o.y * inv), Pair16<T>::pack(o.z * inv, o.w * inv))
                      : make_uint2(0, 0);
         if (p.lse && lane == 0)
-            p.lse[at * p.Hq + head] = sees ? (log2f(l) + (top == -INFINITY ? 0.0f : top - kShift<T>)) * kLn2 : -INFINITY;
+            p.lse[at * p.Hq + head] =
+                sees ? (log2f(l) + (top == -INFINITY ? 0.0f : top - kShift<T>)) * kLn2 : -INFINITY;
     }
 }
 

@@ -29,7 +29,8 @@ __device__ __forceinline__ void copy_part(const PageCaches& c, int cache, int sr
     uint4 w[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-        if (at + i * kThreads * 16 < c.page_bytes) w[i] = *reinterpret_cast<const uint4*>(from + at + i * kThreads * 16);
+        if (at + i * kThreads * 16 < c.page_bytes)
+            w[i] = *reinterpret_cast<const uint4*>(from + at + i * kThreads * 16);
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
         if (at + i * kThreads * 16 < c.page_bytes) *reinterpret_cast<uint4*>(to + at + i * kThreads * 16) = w[i];
@@ -38,7 +39,8 @@ __device__ __forceinline__ void copy_part(const PageCaches& c, int cache, int sr
 __device__ __forceinline__ bool inside(int i, int n) { return static_cast<unsigned>(i) < static_cast<unsigned>(n); }
 
 // blockIdx.x: parts of the pages of all caches, a page's side by side
-__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ PageCaches c, const int* src, const int* dst, int64_t first) {
+__global__ void __launch_bounds__(kThreads)
+    copy_pages_kernel(const __grid_constant__ PageCaches c, const int* src, const int* dst, int64_t first) {
     const unsigned parts = static_cast<unsigned>((c.page_bytes + kPart - 1) / kPart);
     const unsigned page = blockIdx.x / parts, cache = page % c.count;
     const int64_t i = first + page / c.count;
@@ -46,7 +48,9 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
     if (inside(s, c.pages) && inside(d, c.pages) && s != d) copy_part(c, cache, s, d, blockIdx.x % parts);
 }
 
-__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PageCaches c, const ForkArgs f, int64_t first) {
+// the same for the pairs' last pages, and for each pair a CTA for its row of the table
+__global__ void __launch_bounds__(kThreads)
+    fork_kernel(const __grid_constant__ PageCaches c, const ForkArgs f, int64_t first) {
     const unsigned parts = static_cast<unsigned>((c.page_bytes + kPart - 1) / kPart);
     const unsigned copies = parts * c.count, of_pair = copies + f.tables;
     const int64_t i = first + blockIdx.x / of_pair;
