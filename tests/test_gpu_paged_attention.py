@@ -138,6 +138,16 @@ def test_the_most_queries_need_not_be_true(w8a8):
         check(o, lse, q, *c.flat(), n, m, True, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("most", [None, 60])
+def test_few_rows_that_are_all_of_one_sequence(w8a8, most):
+    """As many rows as sequences, which single tokens would be."""
+    n, m = [0, 60] + [0] * 58, [40, 700] + [9] * 58
+    c = Paged(m, 16, 2, 64, BF16, 121)
+    q = queries(sum(n), 8, 64, BF16, 122)
+    o, lse = w8a8.paged_attention(q, c.k_pages, c.v_pages, c.table, c.k_lens, cu_q=starts(n), max_queries=most, lse=True)
+    check(o, lse, q, *c.flat(), n, m, True, 0.125)
+
+
 @pytest.mark.parametrize("n", [1, 7, 150])
 def test_pages_outside_the_cache_are_zeros(w8a8, n):
     m, page, d = 900, 48, 128

@@ -974,8 +974,9 @@ w8a8_status w8a8_paged_attention(
     a.o_head = o_head;
     a.scale_log2 = static_cast<float>(scale_log2);
     a.causal = causal != 0;
-    int64_t most = cu_q ? Tq : Tq / batch;
-    if (max_queries > 0 && max_queries < most) most = max_queries;
+    // (no more rows than sequences: single tokens, most likely; it only chooses the kernel)
+    int64_t most = !cu_q ? Tq / batch : Tq <= batch ? 1 : Tq;
+    if (max_queries > 0 && (max_queries < most || (cu_q && Tq <= batch))) most = std::min(max_queries, Tq);
     void* enc = encode_fn();
     if (!enc) return W8A8_ERR_CUDA;
     t_detail[0] = 0;

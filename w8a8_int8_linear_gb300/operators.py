@@ -212,8 +212,8 @@ def paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q=None, max_quer
     outside the cache reads as zeros).  k_lens: int32 [B] keys of each sequence,
     its new tokens (which are in the cache already) included.  cu_q: int32
     [B + 1] first rows of the sequences' queries; without it the rows are B equal
-    parts.  max_queries: the most queries of a sequence, where the host knows it;
-    it only spares the kernel that would serve more.  causal, scale, out and lse as
+    parts.  max_queries: the most queries of a sequence, where the host knows it; it
+    only chooses between kernels (which may round differently).  causal, scale, out and lse as
     in `attention`; rows of no sequence are not written.
 
     The workspace (`paged_attention_workspace()`, 51 MB) is by default one per
