@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(threads_of(G), 3 - G)
     // us against 24).
     const int longest = __reduce_max_sync(0xffffffffu, most);
     int least = max(1, static_cast<int>(sqrt_approx(0.23f * 16 / R * p.join_rounds * longest)));
-    // Over pages few tiles are not cut at all, as a join takes 2 us by itself (3 sequences
-    // of 1 to 130 keys 6.8 us against 8.1, 8 of 300 8.5 against 9.5; one of 500, which is
-    // cut, 9.2 against 10.2).
-    if (kPaged && longest <= 7) least = longest;
+    // Over pages items of few tiles, each with a range to itself, are not cut at all, as a
+    // join takes 2 us by itself (3 sequences of 1 to 130 keys 6.8 us against 8.1, 8 of 300
+    // 8.5 against 9.5; one of 500, which is cut, 9.2 against 10.2).
+    if (kPaged && few && longest <= 7 && __reduce_add_sync(0xffffffffu, items) <= ranges) least = longest;
     int64_t per = max(static_cast<int64_t>(least), quotient(total + ranges - 1, ranges));
     // A CTA whose range ends one item and begins another takes 3 us longer: where
     // there are few tiles, ranges of a few more that start with the items are better

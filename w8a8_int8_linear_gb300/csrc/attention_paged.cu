@@ -138,7 +138,7 @@ cudaError_t launch_paged_attention(const AttentionArgs& args, int max_queries, i
     // 8000 46 against 36).  Groups of more heads than a tile has rows, and caches without
     // keys, have only that kernel.
     const double keys = static_cast<double>(a.batch) * a.Hk * a.max_pages * a.page_size;
-    const bool few = a.expected_rows <= kFewRows || (a.expected_rows <= 2 * kFewRows && keys <= 98304);
+    const bool few = a.expected_rows <= kFewRows || (a.expected_rows <= 2 * kFewRows && keys <= 131072);
     if (few || a.group > kTileRows || a.max_pages == 0)
         return launch_attention_split(a, dtype, num_sms, workspace, encode_fn, st, detail, n);
     uint8_t* at = static_cast<uint8_t*>(workspace) + attention_workspace_bytes(num_sms);
