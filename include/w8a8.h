@@ -460,9 +460,10 @@ W8A8_API w8a8_status w8a8_qk_norm_rotary_append(
  *   k_lens [batch] int32 (device): keys of each sequence, its new tokens'
  *   included (which are in the cache already); clamped to max_pages * page_size.
  *   cu_q as in w8a8_attention.  max_queries: no sequence has more queries (0:
- *   not known; no more rows than sequences are then taken for single tokens).
- *   It only chooses between kernels: it need not be true for the result to be
- *   right, but another choice may round differently.
+ *   not known; with cu_q, a row for each sequence and Tq * Hq / Hk <= 64 are then
+ *   taken for single tokens, anything else for many queries).  It only chooses
+ *   between kernels: it need not be true for the result to be right, but another
+ *   choice may round differently.
  *   workspace: w8a8_paged_attention_workspace_size() bytes, otherwise as in
  *   w8a8_attention (the first w8a8_attention_workspace_zeroed() bytes zero
  *   before its first use).

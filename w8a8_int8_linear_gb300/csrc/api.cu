@@ -974,9 +974,20 @@ w8a8_status w8a8_paged_attention(
     a.o_head = o_head;
     a.scale_log2 = static_cast<float>(scale_log2);
     a.causal = causal != 0;
-    // (no more rows than sequences: single tokens, most likely; it only chooses the kernel)
-    int64_t most = !cu_q ? Tq / batch : Tq <= batch ? 1 : Tq;
-    if (max_queries > 0 && (max_queries < most || (cu_q && Tq <= batch))) most = std::min(max_queries, Tq);
+    // Which kernel serves the call.  As many rows as sequences, without a word about them,
+    // are single tokens, or a chunk in a batch padded with idle sequences.  Taken for single
+    // tokens, a chunk has its keys read again for every 16 packed rows, and taken for a
+    // chunk, single tokens pay for 128 rows each.  Few rows lose little by the first and
+    // much by the second (us, kernel of few queries against that of many, 32 heads on 8 x
+    // 128: a chunk of 16 over 2000 keys 15 against 22, over 33000 88 against 38; 16 single
+    // tokens over up to 300 keys 9 against 19, up to 30000 159 against 167), many rows the
+    // other way round (512 tokens over 33280 keys 1426 against 195, 200 over 2000 53 against
+    // 30; 48 single ones over up to 8192 130 against 141, 256 up to 1000 104 against 140).
+    int64_t most = cu_q ? Tq : Tq / batch;
+    if (max_queries > 0)
+        most = std::min(max_queries, most);
+    else if (cu_q && Tq == batch && Tq * (Hq / Hk) <= 64)
+        most = 1;
     void* enc = encode_fn();
     if (!enc) return W8A8_ERR_CUDA;
     t_detail[0] = 0;

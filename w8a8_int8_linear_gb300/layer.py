@@ -63,7 +63,8 @@ class Int8TransformerLayer(torch.nn.Module):
 
         With page_table (int32 [batch, most pages]) the caches are pages
         [pages, page_size, kv_heads, dim] (`new_pages`), and row i of page g is slot
-        g * page_size + i.  max_queries: as in `paged_attention`."""
+        g * page_size + i.  max_queries: as in `paged_attention`; a step of single tokens
+        with idle sequences among them passes 1."""
         t = x.shape[0]
         qkv = self.qkv(x).view(t, self.heads + 2 * self.kv_heads, self.dim)
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), dim=1)

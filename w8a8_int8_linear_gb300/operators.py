@@ -213,8 +213,11 @@ def paged_attention(Q, k_pages, v_pages, page_table, k_lens, cu_q=None, max_quer
     its new tokens (which are in the cache already) included.  cu_q: int32
     [B + 1] first rows of the sequences' queries; without it the rows are B equal
     parts.  max_queries: the most queries of a sequence, where the host knows it; it
-    only chooses between kernels (which may round differently).  causal, scale, out and lse as
-    in `attention`; rows of no sequence are not written.
+    only chooses between kernels (which may round differently).  A batch of single
+    tokens passes max_queries=1 with its cu_q, or no cu_q where every sequence has a
+    token; otherwise it is served like a chunk in a batch with idle sequences, which
+    looks the same to the host (unless every sequence has a row and Tq * Hq / Hk <= 64).
+    causal, scale, out and lse as in `attention`; rows of no sequence are not written.
 
     The workspace (`paged_attention_workspace()`, 51 MB) is by default one per
     stream, kept until the process ends, and one of its own, in the graph's
