@@ -353,7 +353,8 @@ typedef enum { W8A8_BF16 = 0, W8A8_FP16 = 1, W8A8_FP32 = 2 } w8a8_dtype;
  * weights exp(t) enter the second product rounded to the inputs' type.
  *   Q [Tq,Hq,D], K, V [Tk,Hk,D], O [Tq,Hq,D]: dtype BF16 or FP16, the last
  *   dimension dense, token and head strides in elements (positive multiples of 8
- *   below 2^39); D % 8 == 0 and D <= 128, Hq % Hk == 0.  O must not overlap the inputs.
+ *   below 2^39); D % 8 == 0 and D <= 128, Hq % Hk == 0, Tq * Hq / Hk and Tk below
+ *   2^31 - 1024.  O must not overlap the inputs.
  *   lse [Tq,Hq] fp32 out or NULL.
  *   cu_q, cu_k [batch+1] int32 (device) or NULL: rows cu[b] .. cu[b+1] are
  *   sequence b's; NULL: batch equal parts of Tq / Tk rows (else
@@ -453,7 +454,7 @@ W8A8_API w8a8_status w8a8_qk_norm_rotary_append(
  * j / page_size].
  *   K_pages, V_pages [pages,page_size,Hk,D]: page, token and head strides in
  *   elements (positive multiples of 8 below 2^39); page_size % 8 == 0, at most
- *   2^20, and max_pages * page_size < 2^31 - 1024.
+ *   2^20, max_pages * page_size and Tq * Hq / Hk below 2^31 - 1024.
  *   page_table [batch,max_pages] int32 (device), rows table_stride apart.  An
  *   entry outside [0, pages) reads as a page of zeros; entries past the last
  *   page of a sequence are not read.

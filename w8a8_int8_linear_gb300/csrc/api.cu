@@ -23,6 +23,9 @@ namespace {
 
 constexpr int64_t kMaxK = 131072;  // 127 * 127 * K must stay below 2^31
 constexpr int kMaxDevices = 64;
+// Rows of queries (times the heads of a group) and of keys: the attention kernels count them
+// in 32 bits, rounded up to whole tiles.
+constexpr int64_t kMostRows = INT32_MAX - 1024;
 
 struct DeviceInfo {
     bool ok;
@@ -623,8 +626,8 @@ w8a8_status w8a8_attention(const void* Q, const void* K, const void* V, void* O,
     if (batch < 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return W8A8_ERR_INVALID_ARG;
     const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;  // the kernels' exponentials are 2^x
     if (!(scale > 0.0f) || !(scale_log2 <= 3.4e38)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
-    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || Tk > INT32_MAX ||
-        batch > INT32_MAX || Tq * (Hq / Hk) > INT32_MAX)
+    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > kMostRows || Tk > kMostRows ||
+        batch > INT32_MAX || Tq * (Hq / Hk) > kMostRows)
         return W8A8_ERR_SHAPE;
     if (batch == 0 || Tq == 0) return W8A8_OK;
     if ((!cu_q && Tq % batch != 0) || (!cu_k && Tk % batch != 0)) return W8A8_ERR_SHAPE;
@@ -920,11 +923,10 @@ w8a8_status w8a8_paged_attention(
         return W8A8_ERR_INVALID_ARG;
     const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;  // the kernels' exponentials are 2^x
     if (!(scale > 0.0f) || !(scale_log2 <= 3.4e38)) return W8A8_ERR_INVALID_ARG;  // also rejects NaN
-    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > INT32_MAX || batch > INT32_MAX ||
-        Tq * (Hq / Hk) > INT32_MAX)
+    if (D % 8 != 0 || D > 128 || Hq % Hk != 0 || Hq > 65535 || Tq > kMostRows || batch > INT32_MAX ||
+        Tq * (Hq / Hk) > kMostRows)
         return W8A8_ERR_SHAPE;
-    if (page_size % 8 != 0 || page_size > (1 << 20) || pages >= INT32_MAX ||
-        max_pages > (INT32_MAX - 1024) / page_size ||  // (a key tile may end behind the last key)
+    if (page_size % 8 != 0 || page_size > (1 << 20) || pages >= INT32_MAX || max_pages > kMostRows / page_size ||
         table_stride > INT32_MAX)
         return W8A8_ERR_SHAPE;
     if (batch == 0 || Tq == 0) return W8A8_OK;
