@@ -492,11 +492,13 @@ W8A8_API w8a8_status w8a8_paged_attention(
  * second sequence like src[i] that can go on by itself: it gets its length and
  * its full pages, and page new_pages[i] for what comes next, into which the
  * last page is copied where it is only partly filled.  A length that fills
- * every page of the row uses no new page.  Nothing happens where src[i] ==
- * dst[i], or where one of the two rows or the new page is outside the table or
- * the cache.  No row may be a destination twice, or a destination and a source;
- * no new page may be used twice or belong to a sequence.  A row may be the
- * source of many.
+ * every page of the row uses no new page (which has to be one all the same).
+ * Nothing happens where src[i] == dst[i], or where one of the two rows or the
+ * new page is outside the table or the cache; so nothing happens, to the table
+ * and the lengths neither, in a call without caches or pages (n_caches or pages
+ * 0), in which every page is outside.  No row may be a destination twice, or a
+ * destination and a source; no new page may be used twice or belong to a
+ * sequence.  A row may be the source of many.
  */
 W8A8_API w8a8_status w8a8_copy_pages(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages,
                                      int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
