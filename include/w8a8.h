@@ -400,6 +400,10 @@ typedef enum {
  * device) of K_cache / V_cache [cache_rows,Hk,D]; a slot outside
  * [0, cache_rows) (-1 for a padding token) stores nothing.  Two tokens with
  * the same slot: either may win, each 16 bytes for themselves.
+ * w8a8_rotary_append_pages: the same for caches in pages, where row r is row
+ * r % page_size of page r / page_size; pages of K_cache / V_cache lie kc_page /
+ * vc_page elements apart (multiples of 8), their rows kc_token / vc_token.
+ * page_size 0: w8a8_rotary_append.
  */
 W8A8_API w8a8_status w8a8_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
                                  int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t q_token, int64_t q_head,
@@ -414,6 +418,13 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
                                         int64_t vc_token, int64_t vc_head, const int64_t* positions,
                                         const int64_t* slots, const double* freqs, float amplitude,
                                         w8a8_rotary_layout layout, void* stream);
+W8A8_API w8a8_status w8a8_rotary_append_pages(
+    const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache, w8a8_dtype dtype, int64_t T,
+    int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t cache_rows, int64_t page_size, int64_t q_token,
+    int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head,
+    int64_t kc_page, int64_t kc_token, int64_t kc_head, int64_t vc_page, int64_t vc_token, int64_t vc_head,
+    const int64_t* positions, const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
+    void* stream);
 
 /*
  * Norms of the heads of Q and K, then their rotary positions, in one pass:
@@ -426,10 +437,8 @@ W8A8_API w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void
  *   k_gamma_head elements apart (0: one row for all; a multiple of 8); NULL: 1.
  *   Q, K, Q_out, K_out, positions, freqs, amplitude, layout: as in w8a8_rotary.
  * w8a8_qk_norm_rotary_append also copies V and writes K and V to rows slots[t]
- * (int64, device) of the caches: row r is row r % page_size of page
- * r / page_size; pages of K_cache / V_cache lie kc_page / vc_page elements
- * apart (multiples of 8), their rows kc_token / vc_token.  page_size 0: caches
- * without pages.  A slot outside [0, cache_rows) stores nothing; two tokens
+ * (int64, device) of the caches, in pages as in w8a8_rotary_append_pages
+ * (page_size 0: caches without pages).  A slot outside [0, cache_rows) stores nothing; two tokens
  * with the same slot: either may win, each 16 bytes for themselves.
  */
 W8A8_API w8a8_status w8a8_qk_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype,

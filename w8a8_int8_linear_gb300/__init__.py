@@ -57,6 +57,7 @@ SIGNATURES = [
     ("w8a8_attention", _I32, [_P] * 8 + [_I32] + [_I64] * 14 + [ctypes.c_float, _I32, _P, _SZ, _P]),
     ("w8a8_rotary", _I32, [_P] * 4 + [_I32] + [_I64] * 13 + [_P, _P, ctypes.c_float, _I32, _I32, _P]),
     ("w8a8_rotary_append", _I32, [_P] * 6 + [_I32] + [_I64] * 18 + [_P, _P, _P, ctypes.c_float, _I32, _P]),
+    ("w8a8_rotary_append_pages", _I32, [_P] * 6 + [_I32] + [_I64] * 21 + [_P, _P, _P, ctypes.c_float, _I32, _P]),
     ("w8a8_qk_norm_rotary", _I32, [_P] * 4 + [_I32] + [_I64] * 13 + [_P, _I64, _P, _I64, ctypes.c_float, _I32, _P, _P,
                                                                     ctypes.c_float, _I32, _P]),
     ("w8a8_qk_norm_rotary_append", _I32, [_P] * 6 + [_I32] + [_I64] * 21 +

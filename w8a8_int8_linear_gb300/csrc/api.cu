@@ -726,6 +726,20 @@ w8a8_status run_rotary(const w8a8::RotaryArgs& a, w8a8_dtype dtype, w8a8_rotary_
     return from_cuda(w8a8::launch_rotary(a, dtype, layout == W8A8_ROTARY_HALF, dev.num_sms, st), "rotary launch");
 }
 
+// Checks of what an append has besides, before check_rotary.
+w8a8_status check_append(int64_t T, int64_t Hq, int64_t Hk, int64_t cache_rows, int64_t page_size, int64_t kc_page,
+                         int64_t vc_page, const int64_t* slots) {
+    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
+    if (Hk <= 0 || page_size < 0) return W8A8_ERR_INVALID_ARG;
+    if (T > 0 && !slots) return W8A8_ERR_INVALID_ARG;
+    if (page_size > INT32_MAX) return W8A8_ERR_SHAPE;
+    if (page_size > 0) {
+        if (kc_page < 0 || vc_page < 0 || kc_page % 8 != 0 || vc_page % 8 != 0) return W8A8_ERR_ALIGNMENT;
+        if ((kc_page == 0 || vc_page == 0) && cache_rows > page_size) return W8A8_ERR_INVALID_ARG;  // on one another
+    }
+    return W8A8_OK;
+}
+
 struct HeadNorms {
     const void* q_gamma;
     int64_t q_gamma_head;
@@ -814,16 +828,20 @@ w8a8_status w8a8_rotary(const void* Q, const void* K, void* Q_out, void* K_out, 
     return run_rotary(a, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
 }
 
-w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache,
-                               w8a8_dtype dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
-                               int64_t cache_rows, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
-                               int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head, int64_t kc_token,
-                               int64_t kc_head, int64_t vc_token, int64_t vc_head, const int64_t* positions,
-                               const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
-                               void* stream) {
-    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
-    if (Hk <= 0) return W8A8_ERR_INVALID_ARG;
-    if (T > 0 && !slots) return W8A8_ERR_INVALID_ARG;
+w8a8_status w8a8_rotary_append_pages(const void* Q, const void* K, const void* V, void* Q_out, void* K_cache,
+                                     void* V_cache, w8a8_dtype dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                     int64_t rot, int64_t cache_rows, int64_t page_size, int64_t q_token,
+                                     int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                                     int64_t qo_token, int64_t qo_head, int64_t kc_page, int64_t kc_token,
+                                     int64_t kc_head, int64_t vc_page, int64_t vc_token, int64_t vc_head,
+                                     const int64_t* positions, const int64_t* slots, const double* freqs,
+                                     float amplitude, w8a8_rotary_layout layout, void* stream) {
+    w8a8_status s = check_append(T, Hq, Hk, cache_rows, page_size, kc_page, vc_page, slots);
+    if (s != W8A8_OK) return s;
+    // pages right behind one another are rows, for which there is the faster kernel
+    if (page_size > 0 && kc_page % page_size == 0 && kc_page / page_size == kc_token && vc_page % page_size == 0 &&
+        vc_page / page_size == vc_token)
+        page_size = 0;
     const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
     w8a8::RotaryArgs a{};
     a.q = {Q, q_token, q_head, hq};
@@ -836,11 +854,26 @@ w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void
     a.slots = slots;
     a.tokens = T;
     a.cache_rows = cache_rows;
+    a.page_size = page_size;
+    a.k_page = kc_page;
+    a.v_page = vc_page;
     a.freqs = freqs;
     a.dim = static_cast<int>(D);
     a.rot = static_cast<int>(rot);
     a.amplitude = amplitude;
     return run_rotary(a, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void* Q_out, void* K_cache, void* V_cache,
+                               w8a8_dtype dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
+                               int64_t cache_rows, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                               int64_t v_token, int64_t v_head, int64_t qo_token, int64_t qo_head, int64_t kc_token,
+                               int64_t kc_head, int64_t vc_token, int64_t vc_head, const int64_t* positions,
+                               const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
+                               void* stream) {
+    return w8a8_rotary_append_pages(Q, K, V, Q_out, K_cache, V_cache, dtype, T, Hq, Hk, D, rot, cache_rows, 0, q_token,
+                                    q_head, k_token, k_head, v_token, v_head, qo_token, qo_head, 0, kc_token, kc_head, 0,
+                                    vc_token, vc_head, positions, slots, freqs, amplitude, layout, stream);
 }
 
 w8a8_status w8a8_qk_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,
@@ -874,14 +907,8 @@ w8a8_status w8a8_qk_norm_rotary_append(
     const void* q_gamma, int64_t q_gamma_head, const void* k_gamma, int64_t k_gamma_head, float eps, w8a8_norm_kind kind,
     const int64_t* positions, const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
     void* stream) {
-    if (Hq > 65535 || Hk > 65535) return W8A8_ERR_SHAPE;
-    if (Hk <= 0 || page_size < 0) return W8A8_ERR_INVALID_ARG;
-    if (T > 0 && !slots) return W8A8_ERR_INVALID_ARG;
-    if (page_size > INT32_MAX) return W8A8_ERR_SHAPE;
-    if (page_size > 0) {
-        if (kc_page < 0 || vc_page < 0 || kc_page % 8 != 0 || vc_page % 8 != 0) return W8A8_ERR_ALIGNMENT;
-        if ((kc_page == 0 || vc_page == 0) && cache_rows > page_size) return W8A8_ERR_INVALID_ARG;  // on one another
-    }
+    w8a8_status s = check_append(T, Hq, Hk, cache_rows, page_size, kc_page, vc_page, slots);
+    if (s != W8A8_OK) return s;
     const int hq = static_cast<int>(Hq), hk = static_cast<int>(Hk);
     w8a8::NormRotaryArgs a{};
     a.r.q = {Q, q_token, q_head, hq};
@@ -898,9 +925,9 @@ w8a8_status w8a8_qk_norm_rotary_append(
     a.r.dim = static_cast<int>(D);
     a.r.rot = static_cast<int>(rot);
     a.r.amplitude = amplitude;
-    a.page_size = page_size;
-    a.k_page = kc_page;
-    a.v_page = vc_page;
+    a.r.page_size = page_size;
+    a.r.k_page = kc_page;
+    a.r.v_page = vc_page;
     const HeadNorms n = {q_gamma, q_gamma_head, k_gamma, k_gamma_head, eps, kind};
     return run_norm_rotary(a, n, dtype, layout, D, rot, static_cast<cudaStream_t>(stream));
 }

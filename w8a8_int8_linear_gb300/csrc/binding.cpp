@@ -362,7 +362,7 @@ PyObject* rotary_append(PyObject* const* a) {
     const Tensor &k = tensor(a[1], "K"), &v = tensor(a[2], "V");
     const Tensor &kc = tensor(a[5], "k_cache"), &vc = tensor(a[6], "v_cache");
     const Heads hk = heads(k, "K", &type), hv = heads(v, "V", &type);
-    const Heads ck = heads(kc, "k_cache", &type), cv = heads(vc, "v_cache", &type);
+    const Cache ck = cache(kc, "k_cache", type, true), cv = cache(vc, "v_cache", type, true);
     if (hk.tokens != hq.tokens || hk.dim != hq.dim) value_error("K must have the tokens and the dim of Q");
     if (k.sizes() != v.sizes() || ck.heads != hk.heads || ck.dim != hk.dim || kc.sizes() != vc.sizes())
         value_error("V must have the shape of K, and both caches its heads and dim");
@@ -371,10 +371,11 @@ PyObject* rotary_append(PyObject* const* a) {
     const c10::cuda::CUDAGuard guard(q.device());
     Tensor q_out;
     const Heads qo = output(a[10], "q_out", q, hq, type, q_out);
-    const w8a8_status s = w8a8_rotary_append(
-        hq.ptr, hk.ptr, hv.ptr, qo.ptr, ck.ptr, cv.ptr, dtype_of(type), hq.tokens, hq.heads, hk.heads, hq.dim, tu.rot,
-        ck.tokens, hq.token, hq.head, hk.token, hk.head, hv.token, hv.head, qo.token, qo.head, ck.token, ck.head, cv.token,
-        cv.head, tu.positions, slots, tu.freqs, static_cast<float>(number(a[9])),
+    const int64_t rows = ck.pages * (kc.dim() == 4 ? ck.page_size : 1);
+    const w8a8_status s = w8a8_rotary_append_pages(
+        hq.ptr, hk.ptr, hv.ptr, qo.ptr, ck.ptr, cv.ptr, dtype_of(type), hq.tokens, hq.heads, hk.heads, hq.dim, tu.rot, rows,
+        ck.page_size, hq.token, hq.head, hk.token, hk.head, hv.token, hv.head, qo.token, qo.head, ck.page,
+        ck.token, ck.head, cv.page, cv.token, cv.head, tu.positions, slots, tu.freqs, static_cast<float>(number(a[9])),
         static_cast<w8a8_rotary_layout>(integer(a[8])), c10::cuda::getCurrentCUDAStream().stream());
     if (s != W8A8_OK) return status(s);
     bump_written(a, arguments);

@@ -109,30 +109,16 @@ __global__ void __launch_bounds__(kThreads, kResident / kThreads)
 
     for (int64_t t = blockIdx.x, turn = 0; t < p.tokens; t += gridDim.x, turn ^= 1) {
         Factors& f = factors[turn];
-        // where this token's K and V go; a slot outside the cache: nowhere
-        int64_t k_at = t * p.k_out.token, v_at = 0;
-        bool store_k = true;
-        if (p.slots) {
-            const int64_t slot = p.slots[t];
-            store_k = slot >= 0 && slot < p.cache_rows;
-            int64_t page = 0, row = slot;
-            if (a.page_size && store_k) {
-                page = (slot >> 31) ? slot / a.page_size
-                                    : static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size);
-                row = slot - page * a.page_size;
-            }
-            k_at = page * a.k_page + row * p.k_out.token;
-            v_at = page * a.v_page + row * p.v_out.token;
-        }
+        const CacheRow at = cache_row<true>(p, t);
         // heads of Q, then of K, then of V
         const int q_heads = p.q.heads, qk_heads = q_heads + p.k.heads;
-        const int heads = store_k ? qk_heads + p.v.heads : q_heads;
+        const int heads = at.store ? qk_heads + p.v.heads : q_heads;
         const T* q_src = static_cast<const T*>(p.q.ptr) + t * p.q.token;
         const T* k_src = static_cast<const T*>(p.k.ptr) + t * p.k.token;
         const T* v_src = static_cast<const T*>(p.v.ptr) + t * p.v.token;
         T* q_dst = static_cast<T*>(const_cast<void*>(p.q_out.ptr)) + t * p.q_out.token;
-        T* k_dst = static_cast<T*>(const_cast<void*>(p.k_out.ptr)) + k_at;
-        T* v_dst = static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + v_at;
+        T* k_dst = static_cast<T*>(const_cast<void*>(p.k_out.ptr)) + at.k;
+        T* v_dst = static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + at.v;
 
         bool ready = false;
         // (all threads of a warp take every pass: the shuffles are theirs together)

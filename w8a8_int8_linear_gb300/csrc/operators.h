@@ -80,6 +80,8 @@ struct RotaryArgs {
     const int64_t* positions;            // [tokens]
     const int64_t* slots;                // [tokens] rows of k_out / v_out, or nullptr: the token's own row
     int64_t tokens, cache_rows;
+    int64_t page_size;                   // rows of a page of k_out and v_out, 0: no pages
+    int64_t k_page, v_page;              // strides of pages
     const double* freqs;                 // [rot / 2]
     int dim, rot, inverse;
     float amplitude;
@@ -96,8 +98,6 @@ struct NormRotaryArgs {
     HeadNorm q_norm, k_norm;
     float eps;
     int layer;
-    int64_t page_size;         // rows of a page of k_out and v_out, 0: no pages
-    int64_t k_page, v_page;    // strides of pages
 };
 cudaError_t launch_norm_rotary(const NormRotaryArgs& a, int dtype, bool half, int num_sms, cudaStream_t st);
 

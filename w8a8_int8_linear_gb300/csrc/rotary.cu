@@ -62,26 +62,20 @@ constexpr int kAtOnce = 3;  // units of a thread in flight
 // take 117 us, the copy bandwidth (126 with the angles in order, where the units
 // of eight neighbouring threads share two banks; 4 units in flight, or the loads
 // after the angles, were 5% slower).
-template <typename T, bool kHalf, int kRotThreads>
+template <typename T, bool kHalf, int kRotThreads, bool kPages>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p) {
     // two pairs each: those of a unit lie a head's units apart, so that the units of
     // neighbouring threads fall into different banks
     __shared__ float4 cs[kMaxPairs / 2];
     const int64_t t = blockIdx.x;
     const int pairs = p.rot >> 1;
-    // the cache row of this token's K and V; outside the cache: not stored
-    int64_t kt = t;
-    bool store_k = true;
-    if (p.slots) {
-        kt = p.slots[t];
-        store_k = kt >= 0 && kt < p.cache_rows;
-    }
+    const CacheRow row = cache_row<kPages>(p, t);
     const int per_head = p.rot >> 4;  // units of a head
-    const int q_units = p.q.heads * per_head, units = q_units + (store_k ? p.k.heads * per_head : 0);
+    const int q_units = p.q.heads * per_head, units = q_units + (row.store ? p.k.heads * per_head : 0);
     const T* q_src = static_cast<const T*>(p.q.ptr) + t * p.q.token;
     const T* k_src = static_cast<const T*>(p.k.ptr) + t * p.k.token;
     T* q_dst = static_cast<T*>(const_cast<void*>(p.q_out.ptr)) + t * p.q_out.token;
-    T* k_dst = static_cast<T*>(const_cast<void*>(p.k_out.ptr)) + kt * p.k_out.token;
+    T* k_dst = static_cast<T*>(const_cast<void*>(p.k_out.ptr)) + row.k;
 
     bool angles = false;
     for (int u0 = threadIdx.x; !angles || u0 < units; u0 += kAtOnce * kRotThreads) {
@@ -144,22 +138,21 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
     };
     const int rest = (p.dim - p.rot) >> 3;
     if (rest) copy(q_src, q_dst, p.q.heads, p.q.head, p.q_out.head, p.rot, rest);
-    if (rest && store_k) copy(k_src, k_dst, p.k.heads, p.k.head, p.k_out.head, p.rot, rest);
-    if (store_k && p.v.ptr)
+    if (rest && row.store) copy(k_src, k_dst, p.k.heads, p.k.head, p.k_out.head, p.rot, rest);
+    if (row.store && p.v.ptr)
         copy(static_cast<const T*>(p.v.ptr) + t * p.v.token,
-             static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + kt * p.v_out.token, p.v.heads, p.v.head, p.v_out.head, 0,
-             p.dim >> 3);
+             static_cast<T*>(const_cast<void*>(p.v_out.ptr)) + row.v, p.v.heads, p.v.head, p.v_out.head, 0, p.dim >> 3);
 }
 
-template <int kRotThreads>
+template <int kRotThreads, bool kPages>
 void launch_threads(const RotaryArgs& a, int dtype, bool half, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>(a.tokens));
     if (dtype == kBf16) {
-        if (half) rotary_kernel<__nv_bfloat16, true, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
-        else rotary_kernel<__nv_bfloat16, false, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
+        if (half) rotary_kernel<__nv_bfloat16, true, kRotThreads, kPages><<<grid, kRotThreads, 0, st>>>(a);
+        else rotary_kernel<__nv_bfloat16, false, kRotThreads, kPages><<<grid, kRotThreads, 0, st>>>(a);
     } else {
-        if (half) rotary_kernel<__half, true, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
-        else rotary_kernel<__half, false, kRotThreads><<<grid, kRotThreads, 0, st>>>(a);
+        if (half) rotary_kernel<__half, true, kRotThreads, kPages><<<grid, kRotThreads, 0, st>>>(a);
+        else rotary_kernel<__half, false, kRotThreads, kPages><<<grid, kRotThreads, 0, st>>>(a);
     }
 }
 
@@ -172,8 +165,18 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool half, int num_sms
     // 32.1), and where eight CTAs of 128 per SM would not hold all tokens (1500 tokens
     // 4.8 against 5.4, 1000 4.1 against 4.0)
     const int units = (a.q.heads + a.k.heads) * (a.rot >> 4);
-    if (units <= 64 * kAtOnce && a.tokens > static_cast<int64_t>(num_sms) * 8) launch_threads<64>(a, dtype, half, st);
-    else launch_threads<128>(a, dtype, half, st);
+    const bool narrow = units <= 64 * kAtOnce && a.tokens > static_cast<int64_t>(num_sms) * 8;
+    // Pages by kernels of their own: the division, and two places of a row, cost 7 to 24%
+    // (4096 tokens of 40 heads on 8 x 128 21.9 us against 20.5, 64 of them 3.5 against 3.2,
+    // 1200 with half of each head turned 8.5 against 6.8), and 3 to 34% where caches of rows
+    // took the same code.
+    if (a.page_size) {
+        if (narrow) launch_threads<64, true>(a, dtype, half, st);
+        else launch_threads<128, true>(a, dtype, half, st);
+    } else {
+        if (narrow) launch_threads<64, false>(a, dtype, half, st);
+        else launch_threads<128, false>(a, dtype, half, st);
+    }
     return cudaGetLastError();
 }
 

@@ -1,8 +1,10 @@
-// The rotary angle, for the kernels that turn heads.
+// The rotary angle, and the cache rows of tokens, for the kernels that turn heads.
 #pragma once
 #include <cuda_runtime.h>
 
 #include <cstdint>
+
+#include "operators.h"
 
 namespace w8a8 {
 namespace {
@@ -30,6 +32,26 @@ __device__ __forceinline__ float half_turns_of(int64_t p, uint64_t step) {
     return static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
 }
 __device__ __forceinline__ float half_turns(int64_t p, double f) { return half_turns_of(p, turn_step(f)); }
+
+// Where K and V of token t go, in elements from k_out and v_out; a slot outside the
+// cache: nowhere.  kPages: caches in pages, where page_size is not 0.
+struct CacheRow {
+    int64_t k, v;
+    bool store;
+};
+template <bool kPages>
+__device__ __forceinline__ CacheRow cache_row(const RotaryArgs& p, int64_t t) {
+    if (!p.slots) return {t * p.k_out.token, 0, true};  // (and no V)
+    const int64_t slot = p.slots[t];
+    const bool store = slot >= 0 && slot < p.cache_rows;
+    if (!kPages) return {slot * p.k_out.token, slot * p.v_out.token, store};
+    int64_t page = 0, row = slot;
+    if (p.page_size && store) {
+        page = (slot >> 31) ? slot / p.page_size : static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
+        row = slot - page * p.page_size;
+    }
+    return {page * p.k_page + row * p.k_out.token, page * p.v_page + row * p.v_out.token, store};
+}
 
 }  // namespace
 }  // namespace w8a8

@@ -62,9 +62,10 @@ class Int8TransformerLayer(torch.nn.Module):
         tokens of each).  Each token sees its sequence's tokens up to itself.
 
         With page_table (int32 [batch, most pages]) the caches are pages
-        [pages, page_size, kv_heads, dim] (`new_pages`), and row i of page g is slot
-        g * page_size + i.  max_queries: as in `paged_attention`; a step of single tokens
-        with idle sequences among them passes 1."""
+        [pages, page_size, kv_heads, dim] (`new_pages`, or views with strides of their
+        own), and row i of page g is slot g * page_size + i.  max_queries: as in
+        `paged_attention`; a step of single tokens with idle sequences among them
+        passes 1."""
         t = x.shape[0]
         qkv = self.qkv(x).view(t, self.heads + 2 * self.kv_heads, self.dim)
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
@@ -74,8 +75,7 @@ class Int8TransformerLayer(torch.nn.Module):
             q = qk_norm_rotary_append(q, k, v, positions, self.frequencies, k_cache, v_cache, slots, self.q_norm,
                                       self.k_norm, self.eps, layout=self.layout, amplitude=self.amplitude)
         else:
-            k_rows, v_rows = (c.view(-1, self.kv_heads, self.dim) if c.dim() == 4 else c for c in (k_cache, v_cache))
-            q = rotary_append(q, k, v, positions, self.frequencies, k_rows, v_rows, slots, self.layout, self.amplitude)
+            q = rotary_append(q, k, v, positions, self.frequencies, k_cache, v_cache, slots, self.layout, self.amplitude)
         if page_table is None:
             a = attention(q, k_cache, v_cache, cu_q=cu_q, k_lens=k_lens, batch=batch)
         else:

@@ -157,9 +157,11 @@ def rotary(Q, K, positions, freqs, layout=HALF, amplitude=1.0, inverse=False, q_
 
 def rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, layout=HALF, amplitude=1.0, q_out=None):
     """`rotary` for tokens that join a cache: turns Q and K, and writes K and V
-    of token t to row slots[t] (int64 [T]) of k_cache / v_cache [rows, Hk, D];
-    a slot outside the cache (-1 for a padding token) stores nothing.  Returns
-    the turned Q."""
+    of token t to row slots[t] (int64 [T]) of k_cache / v_cache: rows
+    [rows, Hk, D], or pages [pages, page_size, Hk, D], where row
+    page * page_size + i is row i of a page (any strides, the last dimension
+    dense).  A slot outside the cache (-1 for a padding token) stores nothing.
+    Returns the turned Q."""
     r = (_binding or binding()).rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, _layout(layout),
                                               amplitude, q_out)
     if type(r) is int:
@@ -184,10 +186,9 @@ def qk_norm_rotary(Q, K, positions, freqs, q_gamma=None, k_gamma=None, eps=1e-6,
 def qk_norm_rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, q_gamma=None, k_gamma=None, eps=1e-6,
                           kind=RMS_NORM, layout=HALF, amplitude=1.0, q_out=None):
     """`qk_norm_rotary` for tokens that join a cache: K, normed and turned, and V
-    of token t go to row slots[t] (int64 [T]) of k_cache / v_cache: rows
-    [rows, Hk, D], or pages [pages, page_size, Hk, D], where row
-    page * page_size + i is row i of a page.  A slot outside the cache (-1 for a
-    padding token) stores nothing.  Returns the normed and turned Q."""
+    of token t go to row slots[t] (int64 [T]) of k_cache / v_cache, rows or pages
+    as in `rotary_append`.  A slot outside the cache (-1 for a padding token) stores
+    nothing.  Returns the normed and turned Q."""
     r = (_binding or binding()).qk_norm_rotary_append(Q, K, V, positions, freqs, k_cache, v_cache, slots, q_gamma,
                                                       k_gamma, eps, kind, _layout(layout), amplitude, q_out)
     if type(r) is int:
