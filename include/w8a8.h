@@ -431,8 +431,8 @@ W8A8_API w8a8_status w8a8_rotary_append_pages(
  * every head x [D] of token t becomes
  *   y = x / sqrt(mean(x^2) + eps) * gamma          (kind RMS; LAYER: of x - mean(x))
  * and pair k of y turns as in w8a8_rotary; in binary32 from the input to one
- * rounding of the result.  A head whose squares leave binary32 (elements above
- * 1.8e19, bf16 only) has no defined result.
+ * rounding of the result.  A head whose squares leave binary32 (bf16 only: elements
+ * above 1.8e19, or with eps 0 all below 1e-19) has no defined result.
  *   q_gamma, k_gamma: the type of Q, [D], or a row for each head, q_gamma_head /
  *   k_gamma_head elements apart (0: one row for all; a multiple of 8); NULL: 1.
  *   Q, K, Q_out, K_out, positions, freqs, amplitude, layout: as in w8a8_rotary.

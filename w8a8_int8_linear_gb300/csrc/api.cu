@@ -783,7 +783,8 @@ w8a8_status check_caches(void* const* caches, const int64_t* strides, int64_t n_
     return W8A8_OK;
 }
 
-// As many launches as the caches need.
+// As many launches as the caches need.  (The later ones of a fork read the sources' rows and
+// lengths again, which the first has left alone: no destination is a source.)
 template <typename F>
 w8a8_status for_caches(void* const* caches, const int64_t* strides, int64_t n_caches, int64_t pages, int64_t page_bytes,
                        F launch) {
