@@ -21,7 +21,8 @@ def calls(w8a8, n, m, hq, hk, d, seed, options):
 
 
 @pytest.mark.parametrize("n,batch,m,hq,hk", [
-    (200, 256, 3000, 40, 8), (60, 60, 3000, 8, 2), (64, 64, 5000, 32, 8), (20, 21, 2000, 12, 4), (256, 256, 4000, 4, 4)])
+    (200, 256, 3000, 40, 8), (60, 60, 3000, 8, 2), (64, 64, 5000, 32, 8), (20, 21, 2000, 12, 4),
+    (256, 256, 4000, 4, 4)])
 def test_a_chunk_in_a_padded_batch(w8a8, n, batch, m, hq, hk):
     """One chunk among idle sequences, no more rows than sequences: the kernel of many
     queries, as where the caller says how many there are."""

@@ -873,8 +873,8 @@ w8a8_status w8a8_rotary_append(const void* Q, const void* K, const void* V, void
                                const int64_t* slots, const double* freqs, float amplitude, w8a8_rotary_layout layout,
                                void* stream) {
     return w8a8_rotary_append_pages(Q, K, V, Q_out, K_cache, V_cache, dtype, T, Hq, Hk, D, rot, cache_rows, 0, q_token,
-                                    q_head, k_token, k_head, v_token, v_head, qo_token, qo_head, 0, kc_token, kc_head, 0,
-                                    vc_token, vc_head, positions, slots, freqs, amplitude, layout, stream);
+                                    q_head, k_token, k_head, v_token, v_head, qo_token, qo_head, 0, kc_token, kc_head,
+                                    0, vc_token, vc_head, positions, slots, freqs, amplitude, layout, stream);
 }
 
 w8a8_status w8a8_qk_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, w8a8_dtype dtype, int64_t T,

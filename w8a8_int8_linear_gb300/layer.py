@@ -75,7 +75,8 @@ class Int8TransformerLayer(torch.nn.Module):
             q = qk_norm_rotary_append(q, k, v, positions, self.frequencies, k_cache, v_cache, slots, self.q_norm,
                                       self.k_norm, self.eps, layout=self.layout, amplitude=self.amplitude)
         else:
-            q = rotary_append(q, k, v, positions, self.frequencies, k_cache, v_cache, slots, self.layout, self.amplitude)
+            q = rotary_append(q, k, v, positions, self.frequencies, k_cache, v_cache, slots, self.layout,
+                              self.amplitude)
         if page_table is None:
             a = attention(q, k_cache, v_cache, cu_q=cu_q, k_lens=k_lens, batch=batch)
         else:
